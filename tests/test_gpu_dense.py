@@ -1,0 +1,567 @@
+"""The dense MoE operators (include/msb_dense.h) against plain 64-bit formulas on the GPU.
+
+Tolerances, derived before the first run.  A rounding to bf16 is off by at most 2^-8 of the
+value, one to float32 by 2^-24.  A sum of k products in float32 adds at most one unit of 2^-23
+of the sum of magnitudes A = |x| . |w| per addition: k 2^-23 A (a bound; errors are far
+smaller).  Each test states what it adds to these.
+"""
+import numpy as np
+import pytest
+
+import oracle
+import synth
+from parity import device_layer, from_bf16_tensor, require_gpu, to_bf16_tensor
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = 2.0 ** -8, 2.0 ** -24
+TINY = 2.0 ** -126  # below the normal range values round to multiples of 2^-133 (bf16)
+
+
+@pytest.fixture(scope="module")
+def msb():
+    return require_gpu()
+
+
+@pytest.fixture(autouse=True)
+def checked(msb):
+    """No kernel of the test gave up waiting."""
+    import torch
+    yield
+    torch.cuda.synchronize()
+    msb.dense_check()
+
+
+def rnd(seed, *shape, scale=1.0, dtype=None):
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype or torch.bfloat16)
+
+
+def within(got, want, tol, what=""):
+    err = (got.double() - want).abs()
+    bad = ~(err <= tol)
+    assert not bad.any(), "%s: %d of %d off, worst %.3g where %.3g is allowed" % (
+        what, int(bad.sum()), bad.numel(), float(err[bad].max()), float(tol[bad].min()))
+
+
+def offsets_of(counts, first=0):
+    import torch
+    return torch.tensor(np.concatenate([[first], first + np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+
+
+def product64(x, w, offs, rows):
+    """(sums, sums of magnitudes) of every row with its group's weight [n][k]; zeros for rows
+    of no group, for a row index outside x."""
+    import torch
+    x = x.double()
+    if rows is not None:
+        ok = (rows >= 0) & (rows < x.shape[0])
+        x = torch.where(ok[:, None], x[rows.long().clamp(0, x.shape[0] - 1)], 0.0)
+    out = torch.zeros((x.shape[0], w.shape[1]), dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(out)
+    at = offs.tolist()
+    for e, (lo, hi) in enumerate(zip(at, at[1:])):
+        if hi > lo:
+            we = w[e].double()
+            out[lo:hi], mag[lo:hi] = x[lo:hi] @ we.t(), x[lo:hi].abs() @ we.abs().t()
+    return out, mag
+
+
+def weight(seed, groups, n, k, layout):
+    """bf16 [groups][n][k]: k contiguous (rows padded to 16 bytes), n contiguous, or the down
+    columns of channel records."""
+    if layout == "k":
+        return rnd(seed, groups, n, (k + 7) // 8 * 8, scale=0.1)[:, :, :k]
+    if layout == "n":
+        return rnd(seed, groups, k, (n + 7) // 8 * 8, scale=0.1)[:, :, :n].transpose(1, 2)
+    return rnd(seed, groups, k, 3, (n + 7) // 8 * 8, scale=0.1)[:, :, 2, :n].transpose(1, 2)
+
+
+COUNTS = {"one": [1], "edges": [31, 0, 32, 33, 1, 0], "pieces": [255, 256, 257, 513],
+          "empty": [0, 0, 0], "skew": [0, 700, 3, 0, 0, 64, 65]}
+
+
+@pytest.mark.parametrize("layout", ["k", "n", "records"])
+@pytest.mark.parametrize("counts", list(COUNTS))
+@pytest.mark.parametrize("n,k", [(1, 8), (7, 33), (128, 64), (257, 200), (640, 1000)])
+def test_grouped_matmul(msb, counts, n, k, layout):
+    import torch
+    c = COUNTS[counts]
+    offs, R = offsets_of(c), sum(c)
+    x = rnd(1, R, (k + 7) // 8 * 8)[:, :k]
+    w = weight(2, len(c), n, k, layout)
+    want, mag = product64(x, w, offs, None)
+    for dtype, step in ((torch.bfloat16, BF16), (torch.float32, F32)):
+        got = msb.grouped_matmul(x, w, offs, out_dtype=dtype)
+        assert got.shape == (R, n) and got.dtype == dtype
+        within(got, want, step * want.abs() + k * 2 * F32 * mag + TINY, dtype)
+
+
+@pytest.mark.parametrize("record", [False, True])
+@pytest.mark.parametrize("counts", list(COUNTS))
+@pytest.mark.parametrize("n,k", [(1, 8), (33, 64), (130, 192), (500, 1024)])
+def test_grouped_swiglu(msb, counts, n, k, record):
+    """h = silu(g) u: with |silu'| < 1.1 an error dg, du of the sums moves h by at most
+    1.1 dg |u| + |silu(g)| du + 1.1 dg du; the exponential and the quotient add 2^-20 |h|."""
+    import torch
+    c = COUNTS[counts]
+    offs, R, T = offsets_of(c), sum(c), 50
+    x = rnd(3, T, k)
+    rows = torch.randint(0, T, (R,), device="cuda", dtype=torch.int32)
+    if record:
+        w = rnd(4, len(c), n, 3, k, scale=0.1)[:, :, :2].permute(0, 2, 1, 3)
+    else:
+        w = rnd(4, len(c), 2, n, k, scale=0.1)
+    g, ga = product64(x, w[:, 0], offs, rows)
+    u, ua = product64(x, w[:, 1], offs, rows)
+    dg, du = k * 2 * F32 * ga, k * 2 * F32 * ua
+    s = torch.nn.functional.silu(g)
+    tol = (BF16 + 2.0 ** -20) * (s * u).abs() + 1.1 * dg * u.abs() + s.abs() * du + 1.1 * dg * du + TINY
+    within(msb.grouped_swiglu(x, w, offs, rows=rows), s * u, tol)
+
+
+def test_swiglu_of_extreme_gates(msb):
+    """Gates of +-300: silu is the gate itself and a zero of either sign, never NaN."""
+    import torch
+    x = torch.zeros((2, 8), device="cuda", dtype=torch.bfloat16)
+    x[0, 0], x[1, 0] = 300.0, -300.0
+    w = torch.zeros((1, 2, 3, 8), device="cuda", dtype=torch.bfloat16)
+    w[0, :, :, 0] = 1.0
+    h = msb.grouped_swiglu(x, w).float()
+    assert torch.equal(h[0], torch.full((3,), 90112.0, device="cuda"))  # 300^2 = 90000 in bf16
+    assert torch.equal(h[1], torch.zeros(3, device="cuda"))
+
+
+def test_rows_of_no_group_and_bad_indices(msb):
+    """Rows before the first offset, behind the last and spare rows of out stay as they were; a
+    row index outside x reads zeros; offsets out of order or out of range touch nothing else."""
+    import torch
+    k, n = 128, 96
+    x, w = rnd(5, 40, k), rnd(6, 3, n, k)
+    offs = offsets_of([5, 0, 20], first=7)
+    rows = torch.arange(40, device="cuda", dtype=torch.int32)
+    rows[9], rows[12], rows[13] = -1, 40, 2 ** 31 - 1
+    out = torch.full((50, n), 7.0, device="cuda", dtype=torch.bfloat16)
+    msb.grouped_matmul(x, w, offs, rows=rows, out=out)
+    want, mag = product64(x, w, offs, rows)
+    within(out[7:32], want[7:32], BF16 * want[7:32].abs() + k * 2 * F32 * mag[7:32])
+    assert (out[:7] == 7).all() and (out[32:] == 7).all()
+    assert (out[9] == 0).all() and (out[12] == 0).all() and (out[13] == 0).all()
+    for bad in ([-5, 3, 2, 1000], [2 ** 31 - 1, 0, -2 ** 31, 4], [40, 30, 20, 10]):
+        out.fill_(7.0)
+        msb.grouped_matmul(x, w, torch.tensor(bad, dtype=torch.int32, device="cuda"), rows=rows, out=out)
+        assert (out[40:] == 7).all()
+
+
+def test_wide_pitches_and_strided_views(msb):
+    """x, out and the weights as column slices of wider buffers: nothing outside is read into the
+    result (the rest is NaN) or written."""
+    import torch
+    k, n, R = 72, 40, 70
+    xb = torch.full((R, 128), float("nan"), device="cuda", dtype=torch.bfloat16)
+    wb = torch.full((2, n, 128), float("nan"), device="cuda", dtype=torch.bfloat16)
+    x, w = xb[:, 16:16 + k], wb[:, :, 8:8 + k]
+    x.copy_(rnd(7, R, k)), w.copy_(rnd(8, 2, n, k))
+    offs = offsets_of([33, 37])
+    want, mag = product64(x, w, offs, None)
+    for dtype, step in ((torch.bfloat16, BF16), (torch.float32, F32)):
+        ob = torch.full((R, 60), 5.0, device="cuda", dtype=dtype)
+        msb.grouped_matmul(x, w, offs, out=ob[:, 3:3 + n])
+        within(ob[:, 3:3 + n], want, step * want.abs() + k * 2 * F32 * mag)
+        assert (ob[:, :3] == 5).all() and (ob[:, 3 + n:] == 5).all()
+
+
+def test_many_groups(msb):
+    """512 groups, most of them empty."""
+    import torch
+    rng = np.random.default_rng(1)
+    c = np.where(rng.random(512) < 0.1, rng.integers(1, 40, 512), 0)
+    offs, k, n = offsets_of(c), 64, 130
+    x, w = rnd(9, int(c.sum()), k), rnd(10, 512, n, k)
+    want, mag = product64(x, w, offs, None)
+    within(msb.grouped_matmul(x, w, offs), want, BF16 * want.abs() + k * 2 * F32 * mag)
+
+
+def test_output_offsets_pass_32_bits(msb):
+    """Rows of out on a pitch of 2^26 elements: the last starts 2^32 elements in."""
+    import torch
+    x, w = rnd(11, 65, 64), rnd(12, 1, 8, 64)
+    out = torch.empty((65, 1 << 26), device="cuda", dtype=torch.bfloat16)[:, :8]
+    out.fill_(0)
+    msb.grouped_matmul(x, w, out=out)
+    want, mag = product64(x, w, offsets_of([65]), None)
+    within(out, want, BF16 * want.abs() + 64 * 2 * F32 * mag)
+
+
+# ------------------------------------------------------------------ 8 bits
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("R,k", [(1, 1), (3, 17), (70, 256), (5, 5000), (2, 20000)])
+def test_quantize_int8(msb, R, k, dtype):
+    """Bit for bit the stated float32 steps."""
+    import torch
+    x = rnd(13, R, k, scale=3.0, dtype=getattr(torch, dtype))
+    x[0, 0] = 0
+    q, s = msb.quantize_int8(x)
+    # numpy's float32 quotient is the rounded one (torch multiplies by a rounded reciprocal)
+    xf = x.float().cpu().numpy()
+    big = np.abs(xf).max(1)
+    live = big >= np.float32(2.0 ** -119)
+    safe = np.where(live, big, np.float32(1))
+    np.testing.assert_array_equal(s.cpu().numpy(), np.where(live, safe / np.float32(127), np.float32(0)))
+    inv = np.where(live, np.float32(127) / safe, np.float32(0))
+    np.testing.assert_array_equal(q.cpu().numpy(), np.rint(xf * inv[:, None]).astype(np.int8))
+
+
+def test_quantize_special_rows(msb):
+    import torch
+    x = torch.zeros((6, 40), device="cuda")
+    x[1, 3] = float("inf")
+    x[2, 39] = float("nan")
+    x[3, 0] = 1e-38
+    x[4, 7] = -3e38
+    x[5, :] = 2.0 ** -119
+    q, s = msb.quantize_int8(x)
+    assert (q[:4] == 0).all() and q[4, 7] == -127 and (q[5] == 127).all()
+    assert s[0] == 0 and s[3] == 0 and torch.isnan(s[1]) and torch.isnan(s[2])
+    w = torch.ones((1, 8, 48), device="cuda", dtype=torch.int8)[:, :, :40]
+    y = msb.matmul_int8(q, s, w, torch.ones((1, 8), device="cuda"))
+    assert torch.isnan(y[1:3].float()).all() and (y[0] == 0).all() and (y[3] == 0).all()
+
+
+@pytest.mark.parametrize("counts", list(COUNTS))
+@pytest.mark.parametrize("n,k", [(1, 16), (7, 33), (257, 200), (300, 1040)])
+def test_matmul_int8(msb, counts, n, k):
+    """The sum is exact; float32 of it and two products: 3 x 2^-24, and the output's rounding."""
+    import torch
+    c = COUNTS[counts]
+    offs, R = offsets_of(c), sum(c)
+    g = torch.Generator(device="cuda").manual_seed(14)
+    q = torch.randint(-128, 128, (R, (k + 15) // 16 * 16), device="cuda", generator=g).to(torch.int8)[:, :k]
+    w = torch.randint(-128, 128, (len(c), n, (k + 15) // 16 * 16), device="cuda", generator=g).to(torch.int8)[:, :, :k]
+    qs, ws = rnd(15, R, dtype=torch.float32).abs(), rnd(16, len(c), n, dtype=torch.float32)
+    want, _ = product64(q, w, offs, None)
+    for e, (lo, hi) in enumerate(zip(offs.tolist(), offs.tolist()[1:])):
+        want[lo:hi] *= ws[e].double()
+    want *= qs.double()[:, None]
+    for dtype, step in ((torch.bfloat16, BF16), (torch.float32, 0)):
+        got = msb.matmul_int8(q, qs, w, ws, offs, out_dtype=dtype)
+        within(got, want, (step + 3.1 * F32) * want.abs() + TINY, dtype)
+
+
+def test_matmul_int8_largest_sums(msb):
+    """k = 131056 products of -128 x -128: the sum 2147221504 is below 2^31 and exact."""
+    import torch
+    k = 131056
+    q = torch.full((2, k), -128, device="cuda", dtype=torch.int8)
+    q[1] = 127
+    w = torch.full((1, 3, k), -128, device="cuda", dtype=torch.int8)
+    one = torch.ones(2, device="cuda")
+    y = msb.matmul_int8(q, one, w, torch.ones((1, 3), device="cuda"), out_dtype=torch.float32)
+    want = torch.tensor([128 * 128 * k, -127 * 128 * k], device="cuda", dtype=torch.float64)[:, None].expand(2, 3)
+    within(y, want, F32 * want.abs())
+
+
+@pytest.mark.parametrize("n,k", [(33, 64), (200, 1024)])
+def test_swiglu_int8(msb, n, k):
+    """As the bf16 form with the sums' errors 3 x 2^-24 of the scaled sum."""
+    import torch
+    c = COUNTS["skew"]
+    offs, R, T = offsets_of(c), sum(c), 90
+    x = rnd(17, T, k)
+    w = torch.randint(-127, 128, (len(c), 2, n, k), device="cuda").to(torch.int8)
+    ws = rnd(18, len(c), 2, n, dtype=torch.float32).abs() * 1e-3
+    rows = torch.randint(0, T, (R,), device="cuda", dtype=torch.int32)
+    q, qs = msb.quantize_int8(x)
+    # the integer sums are exact in 64 bits (a sum of zero stays zero); then the scales
+    group = torch.repeat_interleave(torch.arange(len(c), device="cuda"), torch.tensor(c, device="cuda"))
+    g, u = (product64(q, w[:, p], offs, rows)[0] * qs.double()[rows.long(), None] * ws[group, p].double()
+            for p in range(2))
+    s = torch.nn.functional.silu(g)
+    dg, du = 3.1 * F32 * g.abs(), 3.1 * F32 * u.abs()
+    tol = (BF16 + 2.0 ** -20) * (s * u).abs() + 1.1 * dg * u.abs() + s.abs() * du + TINY
+    got = msb.swiglu_int8(x, w, ws, offs, rows=rows)
+    within(got, s * u, tol)
+    assert torch.equal(got, msb.matmul_int8(q, qs, w, ws, offs, rows=rows, swiglu=True))
+
+
+# ------------------------------------------------------------------ routing
+
+def route_ref(l, top_e, renorm, mask):
+    """Plain loops over float64 logits."""
+    T, E = l.shape
+    ids, wts = -np.ones((T, top_e), np.int64), np.zeros((T, top_e))
+    for t in range(T):
+        if mask is not None and not mask[t]:
+            continue
+        v = np.minimum(l[t], np.float64(np.finfo(np.float32).max))
+        cand = [e for e in range(E) if v[e] > -np.inf]
+        best = sorted(cand, key=lambda e: (-v[e], e))[:top_e]
+        if not best:
+            continue
+        p = np.exp(v - v[best[0]])
+        den = p[best].sum() if renorm else p[cand].sum()
+        ids[t, :len(best)], wts[t, :len(best)] = best, p[best] / den
+    pairs = sorted((ids[t, k], t, k) for t in range(T) for k in range(top_e) if ids[t, k] >= 0)
+    rows, pos = -np.ones(T * top_e, np.int64), -np.ones((T, top_e), np.int64)
+    for p, (e, t, k) in enumerate(pairs):
+        rows[p], pos[t, k] = t, p
+    counts = np.bincount([e for e, _, _ in pairs], minlength=E) if pairs else np.zeros(E, np.int64)
+    return ids, wts, np.concatenate([[0], np.cumsum(counts)]), rows, pos
+
+
+@pytest.mark.parametrize("T", [0, 1, 33, 64, 65, 700])
+@pytest.mark.parametrize("E,K", [(1, 1), (8, 2), (60, 4), (128, 8), (300, 16), (512, 16)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route(msb, T, E, K, renorm):
+    """Ids and plan exact (logits on a coarse grid: many ties); weights: the difference, the
+    exponential (2 ulp), the sum and the quotient: (E + 8) 2^-24 is a bound, |l - max| 2^-24 more
+    from the rounded difference (below 10 here)."""
+    import torch
+    rng = np.random.default_rng(T + E)
+    l = np.round(rng.standard_normal((T, E)) * 4) / 4
+    if T > 8:
+        l[1], l[2, 1:], l[3, ::2], l[4, 0] = -np.inf, -np.inf, np.nan, np.inf
+        l[5, :], l[6, 0] = np.inf, -np.finfo(np.float32).max
+    mask = rng.random(T) < 0.8 if T % 2 else None
+    for dtype in (torch.float32, torch.bfloat16):
+        lt = torch.tensor(l, device="cuda").to(dtype)
+        mt = None if mask is None else torch.tensor(mask, device="cuda")
+        got = msb.route(lt, K, renorm=renorm, mask=mt)
+        with np.errstate(all="ignore"):
+            ids, wts, offs, rows, pos = route_ref(lt.double().cpu().numpy(), K, renorm, mask)
+        for a, b in ((got.ids, ids), (got.offsets, offs), (got.rows, rows), (got.pos, pos)):
+            np.testing.assert_array_equal(a.cpu().numpy(), b)
+        np.testing.assert_allclose(got.weights.cpu().numpy(), wts, rtol=(E + 20) * F32, atol=1e-38)
+
+
+def test_route_many_tokens(msb):
+    """More pairs per block than one chunk holds; strided logits."""
+    import torch
+    T, E, K = 70000, 24, 16
+    l = rnd(19, T, 40, dtype=torch.float32)[:, 3:3 + E]
+    got = msb.route(l, K)
+    ids = torch.argsort(l, dim=1, descending=True, stable=True)[:, :K]
+    assert torch.equal(got.ids.long(), ids)
+    order = torch.argsort(ids.reshape(-1), stable=True)
+    assert torch.equal(got.rows.long(), order // K)
+    assert torch.equal(got.pos.reshape(-1)[order].long(), torch.arange(T * K, device="cuda"))
+    assert torch.equal(got.offsets[1:].long(), torch.cumsum(torch.bincount(ids.reshape(-1), minlength=E), 0))
+
+
+@pytest.mark.parametrize("d", [1, 100, 2048])
+def test_combine(msb, d):
+    """K products and sums in float32: (K + 1) 2^-24 of the sum of magnitudes, one rounding."""
+    import torch
+    T, K, R = 37, 5, 120
+    pos = torch.randint(-1, R, (T, K), device="cuda", dtype=torch.int32)
+    pos[3], pos[4, 0], pos[5, 1] = -1, R, 2 ** 31 - 1
+    w = rnd(20, T, K, dtype=torch.float32)
+    r = msb.Routing(None, w, None, None, pos)
+    for dtype in (torch.bfloat16, torch.float32):
+        y = rnd(21, R, d + 3, dtype=dtype)[:, :d]
+        ok = ((pos >= 0) & (pos < R))
+        terms = torch.where(ok, w, 0.0).double()[..., None] * y.double()[pos.long().clamp(0, R - 1)]
+        want = terms.sum(1)
+        got = msb.combine(y, r)
+        within(got, want, BF16 * want.abs() + (K + 1) * F32 * terms.abs().sum(1) + TINY)
+        assert (got[3] == 0).all()
+
+
+# ------------------------------------------------------------------ block norm
+
+@pytest.mark.parametrize("R,d", [(1, 1), (4, 64), (3, 433), (70, 1000), (5, 2048), (9, 4096), (2, 8192), (2, 16384)])
+@pytest.mark.parametrize("h32,y32", [(True, False), (False, False), (True, True)])
+@pytest.mark.parametrize("gate", [None, "channel", "token", "full", "row"])
+def test_block_norm(msb, R, d, h32, y32, gate):
+    """Float32 steps: the mean of squares within (d + 2) 2^-24 relative (half of that after the
+    root), a dozen roundings more; h' besides by those of its terms' magnitudes; one rounding of
+    each output."""
+    import torch
+    t = lambda f: torch.float32 if f else torch.bfloat16  # noqa: E731
+    h, y = rnd(22, R, d + 8, scale=4.0, dtype=t(h32))[:, :d], rnd(23, R, d, dtype=t(y32))
+    shape = {None: None, "channel": (d,), "token": (R, 1), "full": (R, d), "row": (1, d)}[gate]
+    post = gate != "full"
+    g = None if shape is None else rnd(24, *shape, dtype=t(gate == "token"))
+    pre, pw = rnd(25, d, dtype=t(y32)), (rnd(26, d, dtype=t(y32)) if gate != "row" and post else None)
+    rms = lambda v: v / (v.square().mean(1, keepdim=True) + 1e-6).sqrt()  # noqa: E731
+    b = rms(y.double()) if post else y.double()
+    b = b if pw is None else b * pw.double()
+    b = b if g is None else b * g.double()
+    hw = 0.5 * h.double() + 0.22 * b
+    mag = 0.5 * h.double().abs() + 0.22 * b.abs()
+    xw = rms(hw) * pre.double()
+    h0 = h.clone()
+    ho, x = msb.block_norm(h, y, h_out=torch.empty_like(h0), pre_weight=pre, post_norm=post, post_weight=pw,
+                           gate=g, skip_scale=0.5, residual_scale=0.22)
+    assert torch.equal(h, h0)
+    eps = (d / 2 + 14) * F32
+    within(ho, hw, (F32 if h32 else BF16) * hw.abs() + eps * mag, "h")
+    # x: the norm sees h' off by eps mag; relative to the row's root mean square
+    scale = (hw.square().mean(1, keepdim=True) + 1e-6).sqrt()
+    far = eps * (mag / scale + 2 * xw.abs() / pre.double().abs().clamp(min=1e-30)
+                 + (mag.square().mean(1, keepdim=True).sqrt() / scale) * rms(hw).abs()) * pre.double().abs()
+    within(x, xw, BF16 * xw.abs() + far + TINY, "x")
+    ho2, x2 = msb.block_norm(h, y, x=torch.empty_like(x), pre_weight=pre, post_norm=post, post_weight=pw, gate=g,
+                             skip_scale=0.5, residual_scale=0.22)
+    assert ho2 is h and torch.equal(h, ho) and torch.equal(x2, x)
+
+
+def test_block_norm_is_residual_rmsnorm(msb):
+    """Without weights, gate and scales it is the decode stack's glue."""
+    import torch
+    h, y = rnd(27, 5, 2048, dtype=torch.float32), rnd(28, 5, 2048)
+    h1, x1 = h.clone(), torch.empty_like(y)
+    msb.residual_rmsnorm(h1, y, x1)
+    h2, x2 = msb.block_norm(h.clone(), y)
+    assert torch.equal(h1, h2)
+    # the two kernels' sums run in different orders: a value may fall on the other side of a rounding
+    within(x2, x1.double(), 2 * BF16 * x1.double().abs())
+    h3, x3 = msb.block_norm(h.clone())
+    assert torch.equal(h3, h)
+
+
+def test_block_norm_special_rows(msb):
+    """A row of zeros gives zeros, NaN and infinity stay in their row."""
+    import torch
+    h, y = rnd(29, 4, 300), rnd(30, 4, 300)
+    h[0], y[0] = 0, 0
+    y[1, 7], h[2, 9] = float("nan"), float("inf")
+    ho, x = msb.block_norm(h, y, post_norm=True)
+    assert (x[0] == 0).all() and (ho[0] == 0).all()
+    assert torch.isnan(x[1].float()).all() and torch.isfinite(x[3].float()).all()
+    assert torch.isinf(ho[2, 9].float()) and torch.isnan(x[2, 9].float()) and (x[2, :9] == 0).all()
+
+
+# ------------------------------------------------------------------ the block
+
+@pytest.mark.parametrize("tokens", [1, 3, 300])
+def test_dense_block_against_the_oracle(msb, tokens):
+    """moe_dense_block against the oracle's dense block on sampled tokens.  Three roundings to
+    bf16 along the way (h, the experts' rows, the output), each 2^-8 at most: 2e-2 relative L2 as
+    for the decode block is far outside."""
+    w = synth.TINY
+    lw = synth.layer_weights(w)
+    lay = oracle.ArrayLayer(lw.gate, lw.up, lw.down, lw.router, lw.lr_a, lw.lr_b)
+    layer = device_layer(w)
+    xb = synth.activations(w, 3, batch=tokens)
+    y = msb.moe_dense_block(to_bf16_tensor(xb), layer)
+    got = oracle.bf16_to_f64(from_bf16_tensor(y))
+    for t in sorted({0, tokens // 2, tokens - 1}):
+        ref = oracle.moe_block(xb[t:t + 1], lay, w.top_e, w.inter, rank=0, mode="dense")["y"][0]
+        rel = np.linalg.norm(got[t] - ref) / np.linalg.norm(ref)
+        assert rel < 2e-2, (t, rel)
+
+
+@pytest.mark.parametrize("workload,tokens", [(synth.TINY, 4), (synth.QWEN30B_BLOCK, 16), (synth.QWEN30B_BLOCK, 256)])
+def test_dense_block_is_the_decode_block(msb, workload, tokens):
+    """The same tokens through moe_sparse_block with k = I and rank 0: each side within the
+    roundings above of the same value (a token whose K-th and next logit are equal to float32
+    accuracy may route differently: none of these)."""
+    w = workload
+    layer = device_layer(w, rank=0)
+    x = to_bf16_tensor(synth.activations(w, 5, batch=tokens))
+    a = msb.moe_dense_block(x, layer).double()
+    b = msb.moe_sparse_block(x, layer, w.inter).double()
+    rel = (a - b).norm(dim=1) / b.norm(dim=1)
+    assert rel.max() < 2e-2, rel.max()
+
+
+def test_dense_block_padded_and_int8(msb):
+    """A padded batch gives each prompt what it gives alone, and zeros for the padding; the 8-bit
+    layer stays within the 8-bit error: each of the two products' operands is off by at most half
+    a step of its row's maximum, 1/254, against typical values of a third of it."""
+    import torch
+    w = synth.QWEN30B_BLOCK
+    layer = device_layer(w, rank=0)
+    x = to_bf16_tensor(synth.activations(w, 6, batch=120))
+    mask = torch.arange(120, device="cuda") % 60 < 47
+    alone = torch.cat([msb.moe_dense_block(x[i:i + 47].contiguous(), layer) for i in (0, 60)])
+    both = msb.moe_dense_block(x, layer, mask=mask)
+    # other group sizes, same sums: the products' order along k does not depend on them
+    assert torch.equal(both[mask], alone)
+    assert (both[~mask] == 0).all()
+    y8 = msb.moe_dense_block(x, msb.Int8Layer.from_packed(layer), mask=mask)
+    rel = (y8.double() - both.double())[mask].norm() / both.double()[mask].norm()
+    assert rel < 0.05, rel
+    assert (y8[~mask] == 0).all()
+
+
+def test_prompt_step_with_norms_captured(msb):
+    """Two layers of a stack, block_norm around moe_dense_block, as a user runs them: eager and
+    replayed from a graph on another stream, the same bits; a second graph beside it does not
+    disturb the first."""
+    import torch
+    w = synth.TINY
+    layer = device_layer(w, rank=0)
+    T = 77
+    hs = [rnd(31 + i, T, w.d, dtype=torch.float32) for i in range(2)]
+    pre, post = rnd(33, w.d), rnd(34, w.d)
+
+    def step(h, ws):
+        h, x = msb.block_norm(h, None, h_out=torch.empty_like(h), pre_weight=pre)
+        for _ in range(2):
+            y = msb.moe_dense_block(x, layer, workspace=ws)
+            h, x = msb.block_norm(h, y, h_out=torch.empty_like(h), pre_weight=pre, post_norm=True,
+                                  post_weight=post, residual_scale=0.5)
+        return h, x
+
+    ws = [msb.DenseWorkspace(layer.dims, T) for _ in range(2)]
+    want = [step(h, ws[0]) for h in hs]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graphs, outs, ins = [], [], []
+    for i in range(2):
+        ins.append(torch.zeros_like(hs[i]))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(step(ins[i], ws[i]))
+        graphs.append(g)
+    for i in range(2):
+        ins[i].copy_(hs[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for (h, x), (hw, xw) in zip(outs, want):
+        assert torch.equal(h, hw) and torch.equal(x, xw)
+
+
+def test_calls_on_another_stream(msb):
+    """Outputs allocated for a call on another stream are ordered for it."""
+    import torch
+    w = synth.TINY
+    layer = device_layer(w, rank=0)
+    x = to_bf16_tensor(synth.activations(w, 9, batch=40))
+    want = msb.moe_dense_block(x, layer)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = msb.moe_dense_block(x, layer, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    with pytest.raises(ValueError):
+        msb.moe_dense_block(x, layer, stream=side.cuda_stream)
+
+
+def test_repeatable(msb):
+    """The same call twice gives the same bits."""
+    import torch
+    w = synth.QWEN30B_BLOCK
+    layer = device_layer(w, rank=0)
+    x = to_bf16_tensor(synth.activations(w, 10, batch=200))
+    assert torch.equal(msb.moe_dense_block(x, layer), msb.moe_dense_block(x, layer))
+
+
+def test_dense_block_ignores_rank(msb):
+    """dims.rank does not matter to the dense block."""
+    import torch
+    w = synth.TINY
+    x = to_bf16_tensor(synth.activations(w, 11, batch=9))
+    a = msb.moe_dense_block(x, device_layer(w))
+    b = msb.moe_dense_block(x, device_layer(w, rank=0))
+    assert torch.equal(a, b)

@@ -23,4 +23,20 @@ from .block import (  # noqa: F401
     sketch_words,
     workspace_size,
 )
+from .dense import (  # noqa: F401
+    DenseWorkspace,
+    Int8Layer,
+    Routing,
+    block_norm,
+    combine,
+    dense_check,
+    grouped_matmul,
+    grouped_swiglu,
+    linear_int8,
+    matmul_int8,
+    moe_dense_block,
+    quantize_int8,
+    route,
+    swiglu_int8,
+)
 from . import checkpoint, lowrank, packfile  # noqa: F401,E402

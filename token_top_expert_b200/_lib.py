@@ -1,4 +1,4 @@
-"""ctypes loader of libmsb.so (the C ABI declared in include/msb.h and include/msb_q4.h).
+"""ctypes loader of libmsb.so (the C ABI declared in include/msb*.h).
 
 Loading fails loudly: there is no fallback implementation of any step.
 """
@@ -30,7 +30,7 @@ MSB_MAX_TOP_E = 16
 MSB_MAX_RANK = 128
 MSB_MAX_BATCH = 256
 
-# every function include/msb.h and include/msb_q4.h declare
+# every function include/msb.h, msb_prep.h, msb_q4.h and msb_dense.h declare
 SYMBOLS = (
     "msb_sketch_words", "msb_alpha_count", "msb_pack", "msb_ternary_rows", "msb_workspace_size",
     "msb_workspace_init", "msb_check", "msb_strerror", "moe_sparse_block",
@@ -38,8 +38,18 @@ SYMBOLS = (
     "moe_sparse_block_noalloc", "msb_noalloc_check", "moe_sparse_block_top_e",
     "moe_sparse_block_host",
     "msb_q4_record_bytes", "msb_pack_q4", "moe_sparse_block_q4",
+    "msb_dense_check", "msb_route_workspace_size", "msb_route", "msb_grouped_matmul",
+    "msb_grouped_swiglu", "msb_int8_quantize", "msb_int8_matmul", "msb_int8_swiglu",
+    "msb_combine", "msb_block_norm", "msb_dense_workspace_size", "moe_dense_block",
+    "moe_dense_block_int8",
 )
 MSB_Q4_GROUP = 64
+MSB_BF16 = 0
+MSB_F32 = 1
+MSB_DENSE_MAX_TOKENS = 1048576
+MSB_GROUPED_MAX_NK = 1048576
+MSB_NORM_MAX_D = 16384
+MSB_INT8_MAX_K = 131056
 
 
 class MsbDims(ctypes.Structure):
@@ -51,6 +61,12 @@ class MsbTrace(ctypes.Structure):
     _fields_ = [("expert_ids", ctypes.c_void_p), ("expert_w", ctypes.c_void_p),
                 ("sel", ctypes.c_void_p), ("sel_count", ctypes.c_void_p),
                 ("union_count", ctypes.c_void_p), ("scores", ctypes.c_void_p)]
+
+
+class MsbGroupWeights(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_group", ctypes.c_int64),
+                ("stride_part", ctypes.c_int64), ("stride_n", ctypes.c_int64),
+                ("stride_k", ctypes.c_int64)]
 
 
 class MsbError(RuntimeError):
@@ -73,7 +89,9 @@ def load() -> ctypes.CDLL:
                           % (LIB_PATH, " --instrumented" if VARIANT == "instr" else ""))
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, U32, SZ, F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t, ctypes.c_float
+    I64 = ctypes.c_int64
     dims_p = ctypes.POINTER(MsbDims)
+    w_p = ctypes.POINTER(MsbGroupWeights)
     trace_p = ctypes.POINTER(MsbTrace)
     sig = {
         "msb_sketch_words": (SZ, [dims_p]),
@@ -98,6 +116,20 @@ def load() -> ctypes.CDLL:
                                          trace_p, U32, P]),
         "moe_sparse_block_host": (I32, [P, P, I32, P, P, P, P, I32, P, P, P, P, dims_p, P, SZ,
                                         U32, P]),
+        "msb_dense_check": (I32, [P]),
+        "msb_route_workspace_size": (SZ, [I32, I32]),
+        "msb_route": (I32, [P, I32, I64, P, I32, I32, I32, I32, P, P, P, P, P, P, SZ, P]),
+        "msb_grouped_matmul": (I32, [P, I64, I32, P, P, I32, I32, w_p, I32, I32, P, I32, I64, P]),
+        "msb_grouped_swiglu": (I32, [P, I64, I32, P, P, I32, I32, w_p, I32, I32, P, I64, P]),
+        "msb_int8_quantize": (I32, [P, I32, I64, I32, I32, P, I64, P, P]),
+        "msb_int8_matmul": (I32, [P, I64, P, I32, P, P, I32, I32, w_p, P, I32, I32, P, I32, I64, P]),
+        "msb_int8_swiglu": (I32, [P, I64, P, I32, P, P, I32, I32, w_p, P, I32, I32, P, I64, P]),
+        "msb_combine": (I32, [P, I32, I64, I32, P, P, I32, I32, I32, P, I64, P]),
+        "msb_block_norm": (I32, [P, I32, I64, P, I32, I64, P, P, I32, I32, P, I32, I64, I64, F32, F32,
+                                 F32, P, I64, P, I64, I32, I32, P]),
+        "msb_dense_workspace_size": (SZ, [dims_p, I32, I32]),
+        "moe_dense_block": (I32, [P, I32, P, P, P, P, dims_p, P, SZ, P]),
+        "moe_dense_block_int8": (I32, [P, I32, P, P, P, P, P, P, P, dims_p, P, SZ, P]),
     }
     if VARIANT == "instr":
         sig["msb_debug_set_marks"] = (I32, [P])

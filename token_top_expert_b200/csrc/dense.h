@@ -1,0 +1,34 @@
+// Host-side launches of the dense operators' small kernels (internal to libmsb).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "msb_dense.h"
+
+namespace msb {
+
+int route_blocks(int tokens);  // blocks of the routing kernels: rows of their histogram
+int launch_route(const void* logits, bool bf16, int64_t ld, const uint8_t* mask, int tokens,
+                 int experts, int top_e, bool renorm, int32_t* ids, float* weights,
+                 int32_t* offsets, int32_t* rows, int32_t* pos, int32_t* hist, cudaStream_t st);
+
+int launch_quantize(const void* x, bool f32, int64_t ldx, int rows, int k, int8_t* q, int64_t ldq,
+                    float* scale, cudaStream_t st);
+
+int launch_combine(const void* y, bool f32, int64_t ldy, int y_rows, const int32_t* pos,
+                   const float* weights, int tokens, int top_e, int d, uint16_t* out, int64_t ldo,
+                   cudaStream_t st);
+
+struct NormArgs {
+  const void *h, *y, *pre, *post, *gate;
+  void* h_out;
+  uint16_t* x;
+  int64_t ldh, ldy, ldh_out, ldx, gate_row, gate_col;
+  int d;
+  bool h_f32, y_f32, w_f32, gate_f32, post_norm;
+  float skip, residual, eps;
+};
+int launch_block_norm(const NormArgs& a, int rows, cudaStream_t st);
+
+}  // namespace msb

@@ -1,0 +1,496 @@
+// Products of ragged groups of rows with their group's weight, bf16 or 8-bit integers:
+//
+//   out[p][n] = sum_k x[row(p)][k] * w[e][n][k]        offsets[e] <= p < offsets[e + 1]
+//
+// or, gated, out[p][j] = silu(g) * u with g, u the products with w[e][0][j] and w[e][1][j].
+//
+// The weights are the 256-row operand of the matrix unit and the rows of a group its N side,
+// so that a group of any size fills the unit's rows: N runs over 32, 64, .. 256 in one kernel
+// (a group of c rows is cut into ceil(c / 256) even pieces).  One row streams its experts'
+// weights; a prompt runs at the matrix unit's rate.
+//
+// One CTA pair per tile (persistent, static order), 10 warps a CTA:
+//   warps 0-3  epilogue: tensor memory -> registers -> scale / SwiGLU -> global
+//   warp 4     issues the matrix instructions (even CTA) into one of two accumulators
+//   warp 5     weights: one or two tensor-map boxes per stage of 128 bytes of k
+//   warps 6-9  rows of x, gathered by 16-byte asynchronous copies into the same swizzle
+#include <cuda.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "grouped.h"
+#include "tc.cuh"
+
+namespace msb {
+
+__device__ uint32_t g_dense_err;  // sticky error word, read by msb_dense_check
+
+namespace {
+
+constexpr int kGroupsMax = MSB_MAX_EXPERTS;
+constexpr int kTileM = 256;       // weight rows per CTA pair
+constexpr int kTileN = 256;       // most rows of x per tile
+constexpr int kStageBytes = 128;  // bytes of k per stage (one swizzle row)
+constexpr int kStages = 6;
+constexpr int kABytes = 128 * kStageBytes;           // one CTA's weight rows
+constexpr int kBBytes = kTileN / 2 * kStageBytes;    // one CTA's rows of x
+constexpr int kThreads = 320;
+constexpr int kRowWarps = 4;
+constexpr int kRowLag = 3;  // stages whose copies may still fly when the next is issued
+
+struct Shared {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full[2], acc_empty[2];
+  uint32_t tmem, dead;
+  int32_t first[kGroupsMax + 1];  // first piece of each group
+  int32_t begin[kGroupsMax + 1];  // first row of each group
+  float scale[4][kTileN];         // 8-bit: scales of the tile's rows of x, per epilogue warp
+};
+constexpr size_t kSmemBytes = (size_t)kStages * (kABytes + kBBytes) + 1024 + sizeof(Shared);
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+
+struct KArgs {
+  const uint8_t* x;  // bytes
+  int64_t pitch;     // bytes between rows of x
+  int32_t x_rows;
+  const int32_t* rows;
+  const int32_t* offsets;
+  int32_t groups, out_rows, n, kbytes, mtiles;
+  const float* x_scale;
+  const float* w_scale;
+  void* out;
+  int64_t ldo;
+};
+
+// A bounded wait.  When it runs out, or another role of this CTA has given up, the caller
+// stops waiting for good and leaves through the common exit.
+__device__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t* dead) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1; i < kSpinLimit; ++i) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if (*(volatile uint32_t*)dead) return false;
+    if ((i & 15u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) break;
+  }
+  *(volatile uint32_t*)dead = 1;
+  atomicOr(&g_dense_err, kErrTimeout);
+  return false;
+}
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, uint32_t* dead) {
+  return try_wait_cluster(bar, parity) || wait_slow(bar, parity, dead);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t* dead) {
+  return __all_sync(0xffffffffu, wait_one(bar, parity, dead));
+}
+
+struct Tile {
+  int group, m, row0, rows;  // rows of x: [row0, row0 + rows), rows <= 256
+};
+
+// Rows and pieces before each group, by one warp: every lane takes a run of groups, a scan
+// over the lanes joins them.  Offsets outside [0, out_rows] or below an earlier one are
+// raised or cut to it, so that no offsets lead outside the buffers.
+__device__ void plan_groups(const KArgs& a, Shared& s, int lane) {
+  const int per = (a.groups + 32) >> 5;  // of groups + 1 offsets
+  const int e0 = lane * per, e1 = min(e0 + per, a.groups + 1);
+  int top = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int o = a.offsets ? a.offsets[e] : e ? a.out_rows : 0;
+    top = max(top, min(o, a.out_rows));
+    s.begin[e] = top;
+  }
+  int above = top;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, above, o);
+    if (lane >= o) above = max(above, v);
+  }
+  above = __shfl_up_sync(0xffffffffu, above, 1);
+  if (lane == 0) above = 0;
+  for (int e = e0; e < e1; ++e) s.begin[e] = max(s.begin[e], above);
+  __syncwarp();
+  auto pieces = [&](int e) {
+    return e < a.groups ? (s.begin[e + 1] - s.begin[e] + kTileN - 1) / kTileN : 0;
+  };
+  int sum = 0;
+  for (int e = e0; e < e1; ++e) sum += pieces(e);
+  int before = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  before -= sum;
+  for (int e = e0; e < e1; ++e) {
+    s.first[e] = before;
+    before += pieces(e);
+  }
+}
+
+// The tile of index t (t < first[groups] * mtiles).  Inside a group eight weight tiles go
+// over all its pieces before the next eight, so that the pairs at work share both operands.
+__device__ __forceinline__ Tile tile_at(const KArgs& a, const Shared& s, int t) {
+  int lo = 0, hi = a.groups;  // first[lo] * mtiles <= t < first[hi] * mtiles
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.first[mid] * a.mtiles <= t) lo = mid; else hi = mid;
+  }
+  const int pieces = s.first[lo + 1] - s.first[lo];
+  const int r = t - s.first[lo] * a.mtiles;
+  const int band = r / (8 * pieces);
+  const int wide = min(8, a.mtiles - 8 * band);
+  const int q = r - band * 8 * pieces;
+  const int piece = q / wide;
+  const int b = s.begin[lo], cnt = s.begin[lo + 1] - b;
+  const int each = ((cnt + pieces - 1) / pieces + 31) & ~31;
+  Tile tile;
+  tile.group = lo;
+  tile.m = 8 * band + q - piece * wide;
+  tile.row0 = b + piece * each;
+  tile.rows = min(each, cnt - piece * each);
+  return tile;
+}
+
+// I8: 8-bit integers (else bf16).  MMAJOR: the weight's n runs contiguously (bf16 only).
+// GATED: rows of the weight tile alternate gate, up.  F32: float output.
+template <bool I8, bool MMAJOR, bool GATED, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap wmap, const KArgs a) {
+  extern __shared__ uint8_t raw[];
+  // stages on 1024-byte boundaries (the swizzle's period); same offset in both CTAs
+  uint8_t* const stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+  Shared& s = *reinterpret_cast<Shared*>(stages + (size_t)kStages * (kABytes + kBBytes));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int nk = (a.kbytes + kStageBytes - 1) / kStageBytes;
+
+  if (warp == 0) {
+    plan_groups(a, s, lane);
+  } else if (warp == 4) {
+    tmem_alloc_pair(&s.tmem, 512);
+  } else if (warp == 5 && lane == 0) {
+    prefetch_map(&wmap);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.full[i], 1 + 2 * kRowWarps);
+      mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.acc_full[i], 1);
+      mbar_init(&s.acc_empty[i], 8);
+    }
+    s.dead = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem;
+  const int tiles = s.first[a.groups] * a.mtiles;
+  bool ok = true;
+
+  if (warp == 5 && lane == 0) {
+    // ------------------------------------------------ weights
+    int st = 0;
+    uint32_t phase = 0;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      const Tile tile = tile_at(a, s, t);
+      for (int i = 0; i < nk; ++i) {
+        if (!(ok = wait_one(&s.empty[st], phase ^ 1, &s.dead))) break;
+        const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
+        if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * kABytes);
+        const uint32_t dst = smem_addr(stages) + st * (kABytes + kBBytes);
+        const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
+        if constexpr (GATED) {
+          tma_load_4d(dst, &wmap, k0, 0, tile.m * 128 + (int)rank * 64, tile.group, bar);
+        } else if constexpr (MMAJOR) {
+          tma_load_3d(dst, &wmap, tile.m * kTileM + (int)rank * 128, k0, tile.group, bar);
+          tma_load_3d(dst + kABytes / 2, &wmap, tile.m * kTileM + (int)rank * 128 + 64, k0,
+                      tile.group, bar);
+        } else {
+          tma_load_3d(dst, &wmap, k0, tile.m * kTileM + (int)rank * 128, tile.group, bar);
+        }
+        if (++st == kStages) st = 0, phase ^= 1;
+      }
+    }
+  } else if (warp == 4 && lane == 0 && rank == 0) {
+    // ------------------------------------------------ matrix instructions of the pair
+    int st = 0, buf = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      const Tile tile = tile_at(a, s, t);
+      const uint32_t idesc = instr_desc(I8 ? 2 : 1, MMAJOR, kTileM, (tile.rows + 31) & ~31);
+      if (!(ok = wait_one(&s.acc_empty[buf], acc_phase ^ 1, &s.dead))) break;
+      tc_fence_after();
+      for (int i = 0; i < nk; ++i) {
+        if (!(ok = wait_one(&s.full[st], phase, &s.dead))) break;
+        tc_fence_after();
+        const uint32_t pa = smem_addr(stages) + st * (kABytes + kBBytes), pb = pa + kABytes;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint64_t da = MMAJOR ? smem_desc(pa + q * 2048, kABytes / 2, 1024)
+                                     : smem_desc(pa + q * 32, 16, 1024);
+          mma_pair<I8>(tmem + buf * kTileN, da, smem_desc(pb + q * 32, 16, 1024), idesc,
+                       i > 0 || q > 0);
+        }
+        mma_commit_pair(&s.empty[st]);
+        if (++st == kStages) st = 0, phase ^= 1;
+      }
+      if (!ok) break;
+      mma_commit_pair(&s.acc_full[buf]);
+      if (++buf == 2) buf = 0, acc_phase ^= 1;
+    }
+  } else if (warp >= 6) {
+    // ------------------------------------------------ rows of x
+    const int i0 = threadIdx.x - 6 * 32;
+    const int chunk = i0 & 7, r0 = i0 >> 3;  // 16-byte piece of the 128, row of each 16
+    int st = 0, arrived = 0, issued = 0, arrive_st = 0;
+    uint32_t phase = 0;
+    auto signal = [&]() {  // the oldest stage's copies are complete: hand it to the pair's issuer
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(map_to(smem_addr(&s.full[arrive_st]), 0));
+      if (++arrive_st == kStages) arrive_st = 0;
+      ++arrived;
+    };
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      const Tile tile = tile_at(a, s, t);
+      const int half = ((tile.rows + 31) & ~31) >> 1;  // this CTA's rows of the tile
+      const uint8_t* src[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const int c = (int)rank * half + p * 16 + r0;
+        int row = -1;
+        if (p * 16 < half && c < tile.rows) {
+          row = a.rows ? a.rows[tile.row0 + c] : tile.row0 + c;
+          if (row >= a.x_rows) row = -1;
+        }
+        src[p] = row < 0 ? nullptr : a.x + (int64_t)row * a.pitch + chunk * 16;
+      }
+      for (int i = 0; i < nk; ++i) {
+        if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
+        const uint32_t dst = smem_addr(stages) + st * (kABytes + kBBytes) + kABytes +
+                             r0 * kStageBytes + ((chunk ^ (r0 & 7)) << 4);
+        const int left = a.kbytes - i * kStageBytes - chunk * 16;
+        const uint32_t valid = left < 0 ? 0 : left > 16 ? 16 : left;
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p * 16 < half) {
+            const bool use = src[p] != nullptr && valid != 0;
+            cp_async16(dst + p * 16 * kStageBytes,
+                       use ? src[p] + (int64_t)i * kStageBytes : a.x, use ? valid : 0);
+          }
+        cp_async_commit();
+        ++issued;
+        if (issued - arrived > kRowLag) {
+          cp_async_wait<kRowLag>();
+          signal();
+        }
+        if (++st == kStages) st = 0, phase ^= 1;
+      }
+    }
+    cp_async_wait<0>();
+    while (ok && arrived < issued) signal();
+  } else if (warp < 4) {
+    // ------------------------------------------------ epilogue
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      const Tile tile = tile_at(a, s, t);
+      // channel of this lane: its row of the weight tile
+      const int wrow = (int)rank * 128 + warp * 32 + lane;
+      const int ch = GATED ? tile.m * 128 + (wrow >> 1) : tile.m * kTileM + wrow;
+      float ws = 1.f;
+      if constexpr (I8) {
+        if (ch < a.n)
+          ws = GATED ? a.w_scale[((int64_t)tile.group * 2 + (lane & 1)) * a.n + ch]
+                     : a.w_scale[(int64_t)tile.group * a.n + ch];
+        __syncwarp();  // the last tile's scales have been read
+        for (int c = lane; c < tile.rows; c += 32) {
+          const int row = a.rows ? a.rows[tile.row0 + c] : tile.row0 + c;
+          s.scale[warp][c] = row >= 0 && row < a.x_rows ? a.x_scale[row] : 0.f;
+        }
+        __syncwarp();
+      }
+      if (!(ok = wait_warp(&s.acc_full[buf], acc_phase, &s.dead))) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(warp * 32) << 16);
+      for (int c0 = 0; c0 < tile.rows; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld32(acc + c0, v);
+        tmem_ld_wait();
+        float f[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          f[c] = I8 ? (float)(int32_t)v[c] * s.scale[warp][c0 + c] * ws : __uint_as_float(v[c]);
+        if constexpr (GATED) {
+          // lanes 2i and 2i + 1 hold gate and up of one channel: the even lane forms the even
+          // columns' values, the odd lane the odd columns'
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const bool odd = lane & 1;
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? f[c] : f[c + 1], 1);
+            const float g = odd ? got : f[c], u = odd ? f[c + 1] : got;
+            const float h = g / (1.f + __expf(-g)) * u;
+            const int col = c0 + c + odd;
+            if (col < tile.rows && ch < a.n)
+              static_cast<uint16_t*>(a.out)[(int64_t)(tile.row0 + col) * a.ldo + ch] =
+                  __bfloat16_as_ushort(__float2bfloat16_rn(h));
+          }
+        } else if (ch < a.n) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c < tile.rows) {
+              const int64_t at = (int64_t)(tile.row0 + c0 + c) * a.ldo + ch;
+              if constexpr (F32)
+                static_cast<float*>(a.out)[at] = f[c];
+              else
+                static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(f[c]));
+            }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(map_to(smem_addr(&s.acc_empty[buf]), 0));
+      if (++buf == 2) buf = 0, acc_phase ^= 1;
+    }
+  }
+  __syncwarp();
+  // A role that gave up may leave copies or instructions in flight: they end within
+  // microseconds; let them, so that none reaches an exited CTA or freed tensor memory.
+  if (*(volatile uint32_t*)&s.dead) {
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = 0; i < 4096 && globaltimer_ns() - t0 < 200000; ++i) __nanosleep(1000);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_free_pair(tmem, 512);
+  }
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = []() -> EncodeFn {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// Tensor map of the weights: {k, n, group} boxes of 128 bytes x 128 rows, {n, k, group} boxes
+// of 64 n x 64 k where n runs contiguously, {k, part, n, group} boxes of 128 bytes x 2 parts x
+// 64 channels for the gated form.  Coordinates outside are filled with zeros.
+bool weight_map(const GroupedArgs& a, CUtensorMap* map) {
+  const EncodeFn encode = encode_fn();
+  if (!encode) return false;
+  const int es = a.i8 ? 1 : 2;
+  const bool mmajor = a.w_k != 1;
+  cuuint64_t dims[4], strides[3];
+  cuuint32_t box[4], ones[4] = {1, 1, 1, 1};
+  int rank = 3;
+  if (a.swiglu) {
+    rank = 4;
+    dims[0] = a.k, dims[1] = 2, dims[2] = a.n, dims[3] = a.groups;
+    strides[0] = a.w_part * es, strides[1] = a.w_n * es, strides[2] = a.w_group * es;
+    box[0] = kStageBytes / es, box[1] = 2, box[2] = 64, box[3] = 1;
+  } else if (mmajor) {
+    dims[0] = a.n, dims[1] = a.k, dims[2] = a.groups;
+    strides[0] = a.w_k * es, strides[1] = a.w_group * es;
+    box[0] = 64, box[1] = 64, box[2] = 1;
+  } else {
+    dims[0] = a.k, dims[1] = a.n, dims[2] = a.groups;
+    strides[0] = a.w_n * es, strides[1] = a.w_group * es;
+    box[0] = kStageBytes / es, box[1] = 128, box[2] = 1;
+  }
+  return encode(map, a.i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                const_cast<void*>(a.w), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool I8, bool MMAJOR, bool GATED, bool F32>
+int launch(const CUtensorMap& map, const KArgs& k, cudaStream_t st) {
+  const auto kernel = grouped_kernel<I8, MMAJOR, GATED, F32>;
+  struct Device {
+    std::once_flag once;
+    cudaError_t rc;
+    int sms;
+  };
+  static Device devices[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MSB_ECUDA;
+  Device& d = devices[dev];
+  std::call_once(d.once, [&] {
+    d.rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (d.rc == cudaSuccess) d.rc = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+  });
+  if (d.rc != cudaSuccess) return MSB_ECUDA;
+  // at most one pair per tile: pieces <= groups + rows / 256
+  const int64_t most = ((int64_t)k.groups + k.out_rows / kTileN) * k.mtiles;
+  const int64_t mine = (int64_t)k.out_rows * k.mtiles;  // and every piece has a row
+  const int pairs = (int)std::min<int64_t>(d.sms / 2, std::min(most, mine));
+  kernel<<<2 * pairs, kThreads, kSmemBytes, st>>>(map, k);
+  return cudaGetLastError() == cudaSuccess ? MSB_OK : MSB_ECUDA;
+}
+
+}  // namespace
+
+int launch_grouped(const GroupedArgs& a, cudaStream_t st) {
+  CUtensorMap map;
+  if (!weight_map(a, &map)) return MSB_ECUDA;
+  const int es = a.i8 ? 1 : 2;
+  KArgs k;
+  k.x = static_cast<const uint8_t*>(a.x);
+  k.pitch = a.ldx * es;
+  k.x_rows = a.x_rows;
+  k.rows = a.rows;
+  k.offsets = a.offsets;
+  k.groups = a.groups;
+  k.out_rows = a.out_rows;
+  k.n = a.n;
+  k.kbytes = a.k * es;
+  k.mtiles = a.swiglu ? (a.n + 127) / 128 : (a.n + kTileM - 1) / kTileM;
+  k.x_scale = a.x_scale;
+  k.w_scale = a.w_scale;
+  k.out = a.out;
+  k.ldo = a.ldo;
+  if (a.i8) {
+    if (a.swiglu) return launch<true, false, true, false>(map, k, st);
+    return a.out_f32 ? launch<true, false, false, true>(map, k, st)
+                     : launch<true, false, false, false>(map, k, st);
+  }
+  if (a.swiglu) return launch<false, false, true, false>(map, k, st);
+  if (a.w_k != 1)
+    return a.out_f32 ? launch<false, true, false, true>(map, k, st)
+                     : launch<false, true, false, false>(map, k, st);
+  return a.out_f32 ? launch<false, false, false, true>(map, k, st)
+                   : launch<false, false, false, false>(map, k, st);
+}
+
+int dense_check(cudaStream_t st) {
+  uint32_t err = 0;
+  const uint32_t zero = 0;
+  if (cudaMemcpyFromSymbolAsync(&err, g_dense_err, 4, 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return MSB_ECUDA;
+  if (err != 0 && (cudaMemcpyToSymbolAsync(g_dense_err, &zero, 4, 0, cudaMemcpyHostToDevice, st) !=
+                       cudaSuccess ||
+                   cudaStreamSynchronize(st) != cudaSuccess))
+    return MSB_ECUDA;
+  return err & kErrTimeout ? MSB_ETIMEOUT : MSB_OK;
+}
+
+}  // namespace msb
