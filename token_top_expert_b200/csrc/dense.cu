@@ -39,8 +39,9 @@ int grouped(GroupedArgs a, const msb_group_weights* w, int32_t out_type, cudaStr
   if (!w->data || (a.i8 && !a.w_scale) || (a.out_rows > 0 && (!a.x || !a.out || (a.i8 && !a.x_scale))))
     return MSB_EINVAL;
   if (!aligned16(a.x) || !aligned16(w->data) || !pitch_ok(a.ldx) || !pitch_ok(a.ldo)) return MSB_EINVAL;
-  if (a.x_rows > 1 && a.ldx * es % 16) return MSB_EINVAL;
+  if (a.x_rows > 1 && (a.ldx < 1 || a.ldx * es % 16)) return MSB_EINVAL;
   if (a.out_rows > 1 && a.ldo < a.n) return MSB_EINVAL;
+  if (!a.rows && a.x_rows < a.out_rows) return MSB_EINVAL;
   a.w = w->data;
   a.w_k = w->stride_k, a.w_n = w->stride_n, a.w_part = w->stride_part, a.w_group = w->stride_group;
   const int parts = a.swiglu ? 2 : 1;

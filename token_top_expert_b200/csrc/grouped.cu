@@ -9,11 +9,12 @@
 // (a group of c rows is cut into ceil(c / 256) even pieces).  One row streams its experts'
 // weights; a prompt runs at the matrix unit's rate.
 //
-// One CTA pair per tile (persistent, static order), 10 warps a CTA:
+// One CTA pair per tile (persistent, static order), 7 warps a CTA:
 //   warps 0-3  epilogue: tensor memory -> registers -> scale / SwiGLU -> global
 //   warp 4     issues the matrix instructions (even CTA) into one of two accumulators
 //   warp 5     weights: one or two tensor-map boxes per stage of 128 bytes of k
-//   warps 6-9  rows of x, gathered by 16-byte asynchronous copies into the same swizzle
+//   warp 6     rows of x: boxes of 16 rows, or gathered four rows to an instruction, a lane
+//              each, the row indices held in registers for the whole tile
 #include <cuda.h>
 
 #include <algorithm>
@@ -35,9 +36,8 @@ constexpr int kStageBytes = 128;  // bytes of k per stage (one swizzle row)
 constexpr int kStages = 6;
 constexpr int kABytes = 128 * kStageBytes;           // one CTA's weight rows
 constexpr int kBBytes = kTileN / 2 * kStageBytes;    // one CTA's rows of x
-constexpr int kThreads = 320;
-constexpr int kRowWarps = 4;
-constexpr int kRowLag = 3;  // stages whose copies may still fly when the next is issued
+constexpr int kThreads = 224;
+constexpr int kNoRow = 0x7fffffff;  // a row index outside any x: the load fills zeros
 
 struct Shared {
   uint64_t full[kStages], empty[kStages];
@@ -51,8 +51,6 @@ constexpr size_t kSmemBytes = (size_t)kStages * (kABytes + kBBytes) + 1024 + siz
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 struct KArgs {
-  const uint8_t* x;  // bytes
-  int64_t pitch;     // bytes between rows of x
   int32_t x_rows;
   const int32_t* rows;
   const int32_t* offsets;
@@ -155,7 +153,8 @@ __device__ __forceinline__ Tile tile_at(const KArgs& a, const Shared& s, int t) 
 // GATED: rows of the weight tile alternate gate, up.  F32: float output.
 template <bool I8, bool MMAJOR, bool GATED, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap wmap, const KArgs a) {
+    grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+                   const KArgs a) {
   extern __shared__ uint8_t raw[];
   // stages on 1024-byte boundaries (the swizzle's period); same offset in both CTAs
   uint8_t* const stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
@@ -171,8 +170,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(&s.tmem, 512);
   } else if (warp == 5 && lane == 0) {
     prefetch_map(&wmap);
+    prefetch_map(&xmap);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&s.full[i], 1 + 2 * kRowWarps);
+      mbar_init(&s.full[i], 1);
       mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -196,10 +196,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     for (int t = pair; ok && t < tiles; t += pairs) {
       const Tile tile = tile_at(a, s, t);
+      const uint32_t bytes = 2 * kABytes + ((tile.rows + 31) & ~31) * kStageBytes;
       for (int i = 0; i < nk; ++i) {
         if (!(ok = wait_one(&s.empty[st], phase ^ 1, &s.dead))) break;
         const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
-        if (rank == 0) mbar_arrive_expect_tx(&s.full[st], 2 * kABytes);
+        if (rank == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
         const uint32_t dst = smem_addr(stages) + st * (kABytes + kBBytes);
         const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
         if constexpr (GATED) {
@@ -241,57 +242,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mma_commit_pair(&s.acc_full[buf]);
       if (++buf == 2) buf = 0, acc_phase ^= 1;
     }
-  } else if (warp >= 6) {
+  } else if (warp == 6) {
     // ------------------------------------------------ rows of x
-    const int i0 = threadIdx.x - 6 * 32;
-    const int chunk = i0 & 7, r0 = i0 >> 3;  // 16-byte piece of the 128, row of each 16
-    int st = 0, arrived = 0, issued = 0, arrive_st = 0;
+    int st = 0;
     uint32_t phase = 0;
-    auto signal = [&]() {  // the oldest stage's copies are complete: hand it to the pair's issuer
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(map_to(smem_addr(&s.full[arrive_st]), 0));
-      if (++arrive_st == kStages) arrive_st = 0;
-      ++arrived;
-    };
     for (int t = pair; ok && t < tiles; t += pairs) {
       const Tile tile = tile_at(a, s, t);
       const int half = ((tile.rows + 31) & ~31) >> 1;  // this CTA's rows of the tile
-      const uint8_t* src[8];
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        const int c = (int)rank * half + p * 16 + r0;
-        int row = -1;
-        if (p * 16 < half && c < tile.rows) {
-          row = a.rows ? a.rows[tile.row0 + c] : tile.row0 + c;
-          if (row >= a.x_rows) row = -1;
-        }
-        src[p] = row < 0 ? nullptr : a.x + (int64_t)row * a.pitch + chunk * 16;
+      const int c = (int)rank * half + lane * 4, left = tile.rows - c;
+      int4 row = make_int4(kNoRow, kNoRow, kNoRow, kNoRow);
+      if (a.rows && lane * 4 < half) {
+        const int32_t* r = a.rows + tile.row0 + c;
+        if (left > 0 && (uint32_t)r[0] < (uint32_t)a.x_rows) row.x = r[0];
+        if (left > 1 && (uint32_t)r[1] < (uint32_t)a.x_rows) row.y = r[1];
+        if (left > 2 && (uint32_t)r[2] < (uint32_t)a.x_rows) row.z = r[2];
+        if (left > 3 && (uint32_t)r[3] < (uint32_t)a.x_rows) row.w = r[3];
       }
       for (int i = 0; i < nk; ++i) {
         if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
-        const uint32_t dst = smem_addr(stages) + st * (kABytes + kBBytes) + kABytes +
-                             r0 * kStageBytes + ((chunk ^ (r0 & 7)) << 4);
-        const int left = a.kbytes - i * kStageBytes - chunk * 16;
-        const uint32_t valid = left < 0 ? 0 : left > 16 ? 16 : left;
-#pragma unroll
-        for (int p = 0; p < 8; ++p)
-          if (p * 16 < half) {
-            const bool use = src[p] != nullptr && valid != 0;
-            cp_async16(dst + p * 16 * kStageBytes,
-                       use ? src[p] + (int64_t)i * kStageBytes : a.x, use ? valid : 0);
-          }
-        cp_async_commit();
-        ++issued;
-        if (issued - arrived > kRowLag) {
-          cp_async_wait<kRowLag>();
-          signal();
+        const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
+        const uint32_t dst = smem_addr(stages) + st * (kABytes + kBBytes) + kABytes;
+        const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
+        if (a.rows) {
+          if (lane * 4 < half) tma_gather4(dst + lane * 4 * kStageBytes, &xmap, k0, row, bar);
+        } else if (lane * 16 < half) {
+          // rows behind the group's last belong to the next group: their columns of the
+          // accumulator are not stored
+          tma_load_2d(dst + lane * 16 * kStageBytes, &xmap, k0, tile.row0 + (int)rank * half + lane * 16, bar);
         }
         if (++st == kStages) st = 0, phase ^= 1;
       }
     }
-    cp_async_wait<0>();
-    while (ok && arrived < issued) signal();
   } else if (warp < 4) {
     // ------------------------------------------------ epilogue
     int buf = 0;
@@ -421,8 +402,20 @@ bool weight_map(const GroupedArgs& a, CUtensorMap* map) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tensor map of x: {k, row}, boxes of 128 bytes x 16 rows, or one row for the gathering load.
+bool rows_map(const GroupedArgs& a, CUtensorMap* map) {
+  const int es = a.i8 ? 1 : 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.k, (cuuint64_t)std::max(a.x_rows, 1)};
+  const cuuint64_t strides[1] = {(cuuint64_t)(a.x_rows > 1 ? a.ldx * es : (a.k * es + 15) / 16 * 16)};
+  const cuuint32_t box[2] = {(cuuint32_t)(kStageBytes / es), a.rows ? 1u : 16u}, ones[2] = {1, 1};
+  return encode_fn()(map, a.i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                     const_cast<void*>(a.x), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool I8, bool MMAJOR, bool GATED, bool F32>
-int launch(const CUtensorMap& map, const KArgs& k, cudaStream_t st) {
+int launch(const CUtensorMap& map, const CUtensorMap& xmap, const KArgs& k, cudaStream_t st) {
   const auto kernel = grouped_kernel<I8, MMAJOR, GATED, F32>;
   struct Device {
     std::once_flag once;
@@ -442,19 +435,17 @@ int launch(const CUtensorMap& map, const KArgs& k, cudaStream_t st) {
   const int64_t most = ((int64_t)k.groups + k.out_rows / kTileN) * k.mtiles;
   const int64_t mine = (int64_t)k.out_rows * k.mtiles;  // and every piece has a row
   const int pairs = (int)std::min<int64_t>(d.sms / 2, std::min(most, mine));
-  kernel<<<2 * pairs, kThreads, kSmemBytes, st>>>(map, k);
+  kernel<<<2 * pairs, kThreads, kSmemBytes, st>>>(map, xmap, k);
   return cudaGetLastError() == cudaSuccess ? MSB_OK : MSB_ECUDA;
 }
 
 }  // namespace
 
 int launch_grouped(const GroupedArgs& a, cudaStream_t st) {
-  CUtensorMap map;
-  if (!weight_map(a, &map)) return MSB_ECUDA;
+  CUtensorMap map, xmap;
+  if (!weight_map(a, &map) || !rows_map(a, &xmap)) return MSB_ECUDA;
   const int es = a.i8 ? 1 : 2;
   KArgs k;
-  k.x = static_cast<const uint8_t*>(a.x);
-  k.pitch = a.ldx * es;
   k.x_rows = a.x_rows;
   k.rows = a.rows;
   k.offsets = a.offsets;
@@ -468,16 +459,16 @@ int launch_grouped(const GroupedArgs& a, cudaStream_t st) {
   k.out = a.out;
   k.ldo = a.ldo;
   if (a.i8) {
-    if (a.swiglu) return launch<true, false, true, false>(map, k, st);
-    return a.out_f32 ? launch<true, false, false, true>(map, k, st)
-                     : launch<true, false, false, false>(map, k, st);
+    if (a.swiglu) return launch<true, false, true, false>(map, xmap, k, st);
+    return a.out_f32 ? launch<true, false, false, true>(map, xmap, k, st)
+                     : launch<true, false, false, false>(map, xmap, k, st);
   }
-  if (a.swiglu) return launch<false, false, true, false>(map, k, st);
+  if (a.swiglu) return launch<false, false, true, false>(map, xmap, k, st);
   if (a.w_k != 1)
-    return a.out_f32 ? launch<false, true, false, true>(map, k, st)
-                     : launch<false, true, false, false>(map, k, st);
-  return a.out_f32 ? launch<false, false, false, true>(map, k, st)
-                   : launch<false, false, false, false>(map, k, st);
+    return a.out_f32 ? launch<false, true, false, true>(map, xmap, k, st)
+                     : launch<false, true, false, false>(map, xmap, k, st);
+  return a.out_f32 ? launch<false, false, false, true>(map, xmap, k, st)
+                   : launch<false, false, false, false>(map, xmap, k, st);
 }
 
 int dense_check(cudaStream_t st) {
