@@ -12,7 +12,7 @@
 // One CTA pair per tile (persistent, static order), 7 warps a CTA:
 //   warps 0-3  epilogue: tensor memory -> registers -> scale / SwiGLU -> global
 //   warp 4     issues the matrix instructions (even CTA) into one of two accumulators
-//   warp 5     weights: one or two tensor-map boxes per stage of 128 bytes of k
+//   warp 5     weights: one, two or eight tensor-map boxes per stage of 128 bytes of k
 //   warp 6     rows of x: boxes of 16 rows, or gathered four rows to an instruction, a lane
 //              each, the row indices held in registers for the whole tile
 #include <cuda.h>
@@ -39,6 +39,10 @@ constexpr int kBBytes = kTileN / 2 * kStageBytes;    // one CTA's rows of x
 constexpr int kThreads = 224;
 constexpr int kNoRow = 0x7fffffff;  // a row index outside any x: the load fills zeros
 
+// Bytes between the staged rows of an epilogue warp's 32 bf16 channels: 64 and 16 more, so that
+// eight rows' 16-byte pieces fall into different banks.
+constexpr int kOutPitch = 80;
+
 struct Shared {
   uint64_t full[kStages], empty[kStages];
   uint64_t acc_full[2], acc_empty[2];
@@ -46,6 +50,7 @@ struct Shared {
   int32_t first[kGroupsMax + 1];  // first piece of each group
   int32_t begin[kGroupsMax + 1];  // first row of each group
   float scale[4][kTileN];         // 8-bit: scales of the tile's rows of x, per epilogue warp
+  alignas(16) uint8_t out[4][32 * kOutPitch];  // 32 rows of an epilogue warp's channels
 };
 constexpr size_t kSmemBytes = (size_t)kStages * (kABytes + kBBytes) + 1024 + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
@@ -59,6 +64,7 @@ struct KArgs {
   const float* w_scale;
   void* out;
   int64_t ldo;
+  int wide;  // out may be written in 16-byte pieces
 };
 
 // A bounded wait.  When it runs out, or another role of this CTA has given up, the caller
@@ -149,8 +155,120 @@ __device__ __forceinline__ Tile tile_at(const KArgs& a, const Shared& s, int t) 
   return tile;
 }
 
+// The accumulator's value as a float; 8-bit: the integer sum times the two scales.
+template <bool I8>
+__device__ __forceinline__ float value(uint32_t v, float row_scale, float scale) {
+  if constexpr (I8) return (float)(int32_t)v * row_scale * scale;
+  return __uint_as_float(v);
+}
+
+// One epilogue warp's 32 channels of the accumulator to float: a lane is a channel.
+template <bool I8>
+__device__ __forceinline__ bool store_f32(const KArgs& a, Shared& s, const Tile& tile, uint32_t tmem, int buf,
+                                          uint32_t phase, uint32_t rank, int warp, int lane) {
+  const int ch = tile.m * kTileM + (int)rank * 128 + warp * 32 + lane;
+  const float ws = I8 && ch < a.n ? a.w_scale[(int64_t)tile.group * a.n + ch] : 1.f;
+  if (!wait_warp(&s.acc_full[buf], phase, &s.dead)) return false;
+  tc_fence_after();
+  for (int c0 = 0; c0 < tile.rows; c0 += 32) {
+    uint32_t v[32];
+    tmem_ld32(tmem + buf * kTileN + ((uint32_t)(warp * 32) << 16) + c0, v);
+    tmem_ld_wait();
+    if (ch < a.n) {
+      float* const out = static_cast<float*>(a.out) + (int64_t)(tile.row0 + c0) * a.ldo + ch;
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        if (c0 + c < tile.rows) out[(int64_t)c * a.ldo] = value<I8>(v[c], s.scale[warp][c0 + c], ws);
+    }
+  }
+  return true;
+}
+
+// One epilogue warp's 32 accumulator rows to bf16: 32 channels, or 16 gated ones.  Channels lie
+// along the lanes of tensor memory and contiguously in the output, so 32 columns (rows of out)
+// at a time are turned through shared memory (transposing 8x8 stores) and leave as 16-byte
+// pieces; element by element where out is not aligned for that or the channels end.
+template <bool I8, bool GATED>
+__device__ __forceinline__ bool store_bf16(const KArgs& a, Shared& s, const Tile& tile, uint32_t tmem, int buf,
+                                           uint32_t phase, uint32_t rank, int warp, int lane) {
+  constexpr int kCh = GATED ? 16 : 32;  // channels of this warp
+  const int ch0 = GATED ? tile.m * 128 + (int)rank * 64 + warp * 16 : tile.m * kTileM + (int)rank * 128 + warp * 32;
+  // scales of the accumulator rows lane / 4 + 8 i
+  float ws[4] = {1.f, 1.f, 1.f, 1.f};
+  if constexpr (I8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ch = ch0 + (GATED ? (i >> 1) * 8 : i * 8) + (lane >> 2);
+      if (ch < a.n)
+        ws[i] = GATED ? a.w_scale[((int64_t)tile.group * 2 + (i & 1)) * a.n + ch]
+                      : a.w_scale[(int64_t)tile.group * a.n + ch];
+    }
+  }
+  if (!wait_warp(&s.acc_full[buf], phase, &s.dead)) return false;
+  tc_fence_after();
+  const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(warp * 32) << 16);
+  uint8_t* const stage = s.out[warp];
+  const int lim = a.n - ch0;  // channels of this warp that exist (may be <= 0)
+  for (int c0 = 0; c0 < tile.rows; c0 += 32) {
+    uint32_t v[2][16];
+    tmem_ld16(acc + c0, v[0]);
+    tmem_ld16(acc + (16u << 16) + c0, v[1]);
+    tmem_ld_wait();
+    __syncwarp();  // the last 32 rows have been read
+    float2 rs[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      rs[j] = I8 ? *reinterpret_cast<const float2*>(&s.scale[warp][c0 + 8 * j + 2 * (lane & 3)])
+                 : make_float2(1.f, 1.f);
+    // matrix j: columns 8 j .. 8 j + 7 of eight channels; its rows (columns) in shared memory
+    const uint32_t dst = smem_addr(stage) + lane * kOutPitch;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t m[2][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float lo0 = value<I8>(v[i][4 * j], rs[j].x, ws[2 * i]);
+        const float lo1 = value<I8>(v[i][4 * j + 1], rs[j].y, ws[2 * i]);
+        const float hi0 = value<I8>(v[i][4 * j + 2], rs[j].x, ws[2 * i + 1]);
+        const float hi1 = value<I8>(v[i][4 * j + 3], rs[j].y, ws[2 * i + 1]);
+        if constexpr (GATED) {
+          m[0][j] = pack_bf16(lo0 / (1.f + __expf(-lo0)) * hi0, lo1 / (1.f + __expf(-lo1)) * hi1);
+        } else {
+          m[0][j] = pack_bf16(lo0, lo1);
+          m[1][j] = pack_bf16(hi0, hi1);
+        }
+      }
+      if constexpr (GATED) {
+        stsm_x4_trans(dst + i * 16, m[0][0], m[0][1], m[0][2], m[0][3]);
+      } else {
+        stsm_x4_trans(dst + i * 32, m[0][0], m[0][1], m[0][2], m[0][3]);
+        stsm_x4_trans(dst + i * 32 + 16, m[1][0], m[1][1], m[1][2], m[1][3]);
+      }
+    }
+    __syncwarp();
+    uint16_t* const out = static_cast<uint16_t*>(a.out) + (int64_t)(tile.row0 + c0) * a.ldo + ch0;
+    const int rows = min(32, tile.rows - c0);
+    if (a.wide && lim >= kCh) {
+      constexpr int kPieces = kCh / 8;  // 16-byte pieces of a row
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) {
+        const int at = q * 32 + lane, row = at / kPieces, piece = at % kPieces;
+        if (row < rows)
+          *reinterpret_cast<uint4*>(out + (int64_t)row * a.ldo + piece * 8) =
+              *reinterpret_cast<const uint4*>(stage + row * kOutPitch + piece * 16);
+      }
+    } else {
+      for (int at = lane; at < rows * kCh; at += 32) {
+        const int row = at / kCh, c = at % kCh;
+        if (c < lim) out[(int64_t)row * a.ldo + c] = *reinterpret_cast<const uint16_t*>(stage + row * kOutPitch + 2 * c);
+      }
+    }
+  }
+  return true;
+}
+
 // I8: 8-bit integers (else bf16).  MMAJOR: the weight's n runs contiguously (bf16 only).
-// GATED: rows of the weight tile alternate gate, up.  F32: float output.
+// GATED: rows of the weight tile alternate in eights, gate and up.  F32: float output.
 template <bool I8, bool MMAJOR, bool GATED, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
@@ -190,7 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int tiles = s.first[a.groups] * a.mtiles;
   bool ok = true;
 
-  if (warp == 5 && lane == 0) {
+  if (warp == 5) {
     // ------------------------------------------------ weights
     int st = 0;
     uint32_t phase = 0;
@@ -198,19 +316,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Tile tile = tile_at(a, s, t);
       const uint32_t bytes = 2 * kABytes + ((tile.rows + 31) & ~31) * kStageBytes;
       for (int i = 0; i < nk; ++i) {
-        if (!(ok = wait_one(&s.empty[st], phase ^ 1, &s.dead))) break;
+        if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
         const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
-        if (rank == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
         const uint32_t dst = smem_addr(stages) + st * (kABytes + kBBytes);
         const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
         if constexpr (GATED) {
-          tma_load_4d(dst, &wmap, k0, 0, tile.m * 128 + (int)rank * 64, tile.group, bar);
+          // eight channels' gate rows, then their up rows: 16 rows of the tile
+          if (lane < 8)
+            tma_load_4d(dst + lane * 16 * kStageBytes, &wmap, k0, tile.m * 128 + (int)rank * 64 + lane * 8, 0,
+                        tile.group, bar);
         } else if constexpr (MMAJOR) {
-          tma_load_3d(dst, &wmap, tile.m * kTileM + (int)rank * 128, k0, tile.group, bar);
-          tma_load_3d(dst + kABytes / 2, &wmap, tile.m * kTileM + (int)rank * 128 + 64, k0,
-                      tile.group, bar);
+          if (lane < 2)
+            tma_load_3d(dst + lane * (kABytes / 2), &wmap, tile.m * kTileM + (int)rank * 128 + lane * 64, k0,
+                        tile.group, bar);
         } else {
-          tma_load_3d(dst, &wmap, k0, tile.m * kTileM + (int)rank * 128, tile.group, bar);
+          if (lane == 0)
+            tma_load_3d(dst, &wmap, k0, tile.m * kTileM + (int)rank * 128, tile.group, bar);
         }
         if (++st == kStages) st = 0, phase ^= 1;
       }
@@ -279,58 +401,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;
     for (int t = pair; ok && t < tiles; t += pairs) {
       const Tile tile = tile_at(a, s, t);
-      // channel of this lane: its row of the weight tile
-      const int wrow = (int)rank * 128 + warp * 32 + lane;
-      const int ch = GATED ? tile.m * 128 + (wrow >> 1) : tile.m * kTileM + wrow;
-      float ws = 1.f;
       if constexpr (I8) {
-        if (ch < a.n)
-          ws = GATED ? a.w_scale[((int64_t)tile.group * 2 + (lane & 1)) * a.n + ch]
-                     : a.w_scale[(int64_t)tile.group * a.n + ch];
         __syncwarp();  // the last tile's scales have been read
         for (int c = lane; c < tile.rows; c += 32) {
           const int row = a.rows ? a.rows[tile.row0 + c] : tile.row0 + c;
-          s.scale[warp][c] = row >= 0 && row < a.x_rows ? a.x_scale[row] : 0.f;
+          s.scale[warp][c] = (uint32_t)row < (uint32_t)a.x_rows ? a.x_scale[row] : 0.f;
         }
         __syncwarp();
       }
-      if (!(ok = wait_warp(&s.acc_full[buf], acc_phase, &s.dead))) break;
-      tc_fence_after();
-      const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(warp * 32) << 16);
-      for (int c0 = 0; c0 < tile.rows; c0 += 32) {
-        uint32_t v[32];
-        tmem_ld32(acc + c0, v);
-        tmem_ld_wait();
-        float f[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c)
-          f[c] = I8 ? (float)(int32_t)v[c] * s.scale[warp][c0 + c] * ws : __uint_as_float(v[c]);
-        if constexpr (GATED) {
-          // lanes 2i and 2i + 1 hold gate and up of one channel: the even lane forms the even
-          // columns' values, the odd lane the odd columns'
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const bool odd = lane & 1;
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? f[c] : f[c + 1], 1);
-            const float g = odd ? got : f[c], u = odd ? f[c + 1] : got;
-            const float h = g / (1.f + __expf(-g)) * u;
-            const int col = c0 + c + odd;
-            if (col < tile.rows && ch < a.n)
-              static_cast<uint16_t*>(a.out)[(int64_t)(tile.row0 + col) * a.ldo + ch] =
-                  __bfloat16_as_ushort(__float2bfloat16_rn(h));
-          }
-        } else if (ch < a.n) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c0 + c < tile.rows) {
-              const int64_t at = (int64_t)(tile.row0 + c0 + c) * a.ldo + ch;
-              if constexpr (F32)
-                static_cast<float*>(a.out)[at] = f[c];
-              else
-                static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(f[c]));
-            }
-        }
-      }
+      if constexpr (F32)
+        ok = store_f32<I8>(a, s, tile, tmem, buf, acc_phase, rank, warp, lane);
+      else
+        ok = store_bf16<I8, GATED>(a, s, tile, tmem, buf, acc_phase, rank, warp, lane);
+      if (!ok) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_cluster(map_to(smem_addr(&s.acc_empty[buf]), 0));
@@ -372,8 +455,8 @@ EncodeFn encode_fn() {
 }
 
 // Tensor map of the weights: {k, n, group} boxes of 128 bytes x 128 rows, {n, k, group} boxes
-// of 64 n x 64 k where n runs contiguously, {k, part, n, group} boxes of 128 bytes x 2 parts x
-// 64 channels for the gated form.  Coordinates outside are filled with zeros.
+// of 64 n x 64 k where n runs contiguously, {k, n, part, group} boxes of 128 bytes x 8
+// channels x 2 parts for the gated form.  Coordinates outside are filled with zeros.
 bool weight_map(const GroupedArgs& a, CUtensorMap* map) {
   const EncodeFn encode = encode_fn();
   if (!encode) return false;
@@ -384,9 +467,9 @@ bool weight_map(const GroupedArgs& a, CUtensorMap* map) {
   int rank = 3;
   if (a.swiglu) {
     rank = 4;
-    dims[0] = a.k, dims[1] = 2, dims[2] = a.n, dims[3] = a.groups;
-    strides[0] = a.w_part * es, strides[1] = a.w_n * es, strides[2] = a.w_group * es;
-    box[0] = kStageBytes / es, box[1] = 2, box[2] = 64, box[3] = 1;
+    dims[0] = a.k, dims[1] = a.n, dims[2] = 2, dims[3] = a.groups;
+    strides[0] = a.w_n * es, strides[1] = a.w_part * es, strides[2] = a.w_group * es;
+    box[0] = kStageBytes / es, box[1] = 8, box[2] = 2, box[3] = 1;
   } else if (mmajor) {
     dims[0] = a.n, dims[1] = a.k, dims[2] = a.groups;
     strides[0] = a.w_k * es, strides[1] = a.w_group * es;
@@ -458,6 +541,7 @@ int launch_grouped(const GroupedArgs& a, cudaStream_t st) {
   k.w_scale = a.w_scale;
   k.out = a.out;
   k.ldo = a.ldo;
+  k.wide = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && (a.ldo % 8 == 0 || a.out_rows == 1);
   if (a.i8) {
     if (a.swiglu) return launch<true, false, true, false>(map, xmap, k, st);
     return a.out_f32 ? launch<true, false, false, true>(map, xmap, k, st)
