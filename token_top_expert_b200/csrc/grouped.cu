@@ -9,12 +9,13 @@
 // (a group of c rows is cut into ceil(c / 256) even pieces).  One row streams its experts'
 // weights; a prompt runs at the matrix unit's rate.
 //
-// One CTA pair per tile (persistent, static order), 7 warps a CTA:
+// One CTA pair per tile (persistent, static order), 10 warps a CTA:
 //   warps 0-3  epilogue: tensor memory -> registers -> scale / SwiGLU -> global
 //   warp 4     issues the matrix instructions (even CTA) into one of two accumulators
 //   warp 5     weights: one, two or eight tensor-map boxes per stage of 128 bytes of k
-//   warp 6     rows of x: boxes of 16 rows, or gathered four rows to an instruction, a lane
-//              each, the row indices held in registers for the whole tile
+//   warps 6-9  rows of x: boxes of 128, 64, 32 and 16 rows (warp 6), or gathered four rows to an
+//              instruction, an eighth of each warp's instructions at a time (one thread issues
+//              an instruction in about 60 cycles, and 128 rows take 32 of them)
 #include <cuda.h>
 
 #include <algorithm>
@@ -36,7 +37,7 @@ constexpr int kStageBytes = 128;  // bytes of k per stage (one swizzle row)
 constexpr int kStages = 6;
 constexpr int kABytes = 128 * kStageBytes;           // one CTA's weight rows
 constexpr int kBBytes = kTileN / 2 * kStageBytes;    // one CTA's rows of x
-constexpr int kThreads = 224;
+constexpr int kThreads = 320;
 constexpr int kNoRow = 0x7fffffff;  // a row index outside any x: the load fills zeros
 
 // Bytes between the staged rows of an epilogue warp's 32 bf16 channels: 64 and 16 more, so that
@@ -65,6 +66,11 @@ struct KArgs {
   void* out;
   int64_t ldo;
   int wide;  // out may be written in 16-byte pieces
+};
+
+// Tensor maps of x: boxes of 16 << i rows, or of one row (map 0) for the gathering load.
+struct RowMaps {
+  CUtensorMap map[4];
 };
 
 // A bounded wait.  When it runs out, or another role of this CTA has given up, the caller
@@ -271,7 +277,7 @@ __device__ __forceinline__ bool store_bf16(const KArgs& a, Shared& s, const Tile
 // GATED: rows of the weight tile alternate in eights, gate and up.  F32: float output.
 template <bool I8, bool MMAJOR, bool GATED, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+    grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ RowMaps xmaps,
                    const KArgs a) {
   extern __shared__ uint8_t raw[];
   // stages on 1024-byte boundaries (the swizzle's period); same offset in both CTAs
@@ -288,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(&s.tmem, 512);
   } else if (warp == 5 && lane == 0) {
     prefetch_map(&wmap);
-    prefetch_map(&xmap);
+    for (int i = 0; i < (a.rows ? 1 : 4); ++i) prefetch_map(&xmaps.map[i]);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.empty[i], 1);
@@ -364,34 +370,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mma_commit_pair(&s.acc_full[buf]);
       if (++buf == 2) buf = 0, acc_phase ^= 1;
     }
-  } else if (warp == 6) {
-    // ------------------------------------------------ rows of x
+  } else if (warp >= 6 && a.rows && lane == 0) {
+    // ------------------------------------------------ rows of x, gathered
     int st = 0;
     uint32_t phase = 0;
     for (int t = pair; ok && t < tiles; t += pairs) {
       const Tile tile = tile_at(a, s, t);
       const int half = ((tile.rows + 31) & ~31) >> 1;  // this CTA's rows of the tile
-      const int c = (int)rank * half + lane * 4, left = tile.rows - c;
-      int4 row = make_int4(kNoRow, kNoRow, kNoRow, kNoRow);
-      if (a.rows && lane * 4 < half) {
-        const int32_t* r = a.rows + tile.row0 + c;
-        if (left > 0 && (uint32_t)r[0] < (uint32_t)a.x_rows) row.x = r[0];
-        if (left > 1 && (uint32_t)r[1] < (uint32_t)a.x_rows) row.y = r[1];
-        if (left > 2 && (uint32_t)r[2] < (uint32_t)a.x_rows) row.z = r[2];
-        if (left > 3 && (uint32_t)r[3] < (uint32_t)a.x_rows) row.w = r[3];
+      // this warp takes four rows of every 16
+      int4 row[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        row[q] = make_int4(kNoRow, kNoRow, kNoRow, kNoRow);
+        const int c = (int)rank * half + q * 16 + (warp - 6) * 4, left = tile.rows - c;
+        if (q * 16 < half) {
+          const int32_t* r = a.rows + tile.row0 + c;
+          if (left > 0 && (uint32_t)r[0] < (uint32_t)a.x_rows) row[q].x = r[0];
+          if (left > 1 && (uint32_t)r[1] < (uint32_t)a.x_rows) row[q].y = r[1];
+          if (left > 2 && (uint32_t)r[2] < (uint32_t)a.x_rows) row[q].z = r[2];
+          if (left > 3 && (uint32_t)r[3] < (uint32_t)a.x_rows) row[q].w = r[3];
+        }
       }
       for (int i = 0; i < nk; ++i) {
-        if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
+        if (!(ok = wait_one(&s.empty[st], phase ^ 1, &s.dead))) break;
+        const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
+        const uint32_t dst = smem_addr(stages) + st * (kABytes + kBBytes) + kABytes + (warp - 6) * 4 * kStageBytes;
+        const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q * 16 < half) tma_gather4(dst + q * 16 * kStageBytes, &xmaps.map[0], k0, row[q], bar);
+        if (++st == kStages) st = 0, phase ^= 1;
+      }
+    }
+  } else if (warp == 6 && !a.rows && lane == 0) {
+    // ------------------------------------------------ rows of x, as they lie
+    int st = 0;
+    uint32_t phase = 0;
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      const Tile tile = tile_at(a, s, t);
+      const int half = ((tile.rows + 31) & ~31) >> 1;
+      const int row0 = tile.row0 + (int)rank * half;
+      for (int i = 0; i < nk; ++i) {
+        if (!(ok = wait_one(&s.empty[st], phase ^ 1, &s.dead))) break;
         const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
         const uint32_t dst = smem_addr(stages) + st * (kABytes + kBBytes) + kABytes;
         const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
-        if (a.rows) {
-          if (lane * 4 < half) tma_gather4(dst + lane * 4 * kStageBytes, &xmap, k0, row, bar);
-        } else if (lane * 16 < half) {
-          // rows behind the group's last belong to the next group: their columns of the
-          // accumulator are not stored
-          tma_load_2d(dst + lane * 16 * kStageBytes, &xmap, k0, tile.row0 + (int)rank * half + lane * 16, bar);
-        }
+        // rows behind the group's last belong to the next group: their columns of the
+        // accumulator are not stored
+#pragma unroll
+        for (int b = 3; b >= 0; --b)
+          if (half & (16 << b)) {
+            const int done = half & ~((32 << b) - 1);
+            tma_load_2d(dst + done * kStageBytes, &xmaps.map[b], k0, row0 + done, bar);
+          }
         if (++st == kStages) st = 0, phase ^= 1;
       }
     }
@@ -485,20 +516,24 @@ bool weight_map(const GroupedArgs& a, CUtensorMap* map) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tensor map of x: {k, row}, boxes of 128 bytes x 16 rows, or one row for the gathering load.
-bool rows_map(const GroupedArgs& a, CUtensorMap* map) {
+// Tensor maps of x: {k, row}, boxes of 128 bytes.
+bool row_maps(const GroupedArgs& a, RowMaps* maps) {
   const int es = a.i8 ? 1 : 2;
   const cuuint64_t dims[2] = {(cuuint64_t)a.k, (cuuint64_t)std::max(a.x_rows, 1)};
   const cuuint64_t strides[1] = {(cuuint64_t)(a.x_rows > 1 ? a.ldx * es : (a.k * es + 15) / 16 * 16)};
-  const cuuint32_t box[2] = {(cuuint32_t)(kStageBytes / es), a.rows ? 1u : 16u}, ones[2] = {1, 1};
-  return encode_fn()(map, a.i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                     const_cast<void*>(a.x), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  for (int i = 0; i < (a.rows ? 1 : 4); ++i) {
+    const cuuint32_t box[2] = {(cuuint32_t)(kStageBytes / es), a.rows ? 1u : 16u << i}, ones[2] = {1, 1};
+    if (encode_fn()(&maps->map[i], a.i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                    const_cast<void*>(a.x), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  return true;
 }
 
 template <bool I8, bool MMAJOR, bool GATED, bool F32>
-int launch(const CUtensorMap& map, const CUtensorMap& xmap, const KArgs& k, cudaStream_t st) {
+int launch(const CUtensorMap& map, const RowMaps& xmaps, const KArgs& k, cudaStream_t st) {
   const auto kernel = grouped_kernel<I8, MMAJOR, GATED, F32>;
   struct Device {
     std::once_flag once;
@@ -518,15 +553,16 @@ int launch(const CUtensorMap& map, const CUtensorMap& xmap, const KArgs& k, cuda
   const int64_t most = ((int64_t)k.groups + k.out_rows / kTileN) * k.mtiles;
   const int64_t mine = (int64_t)k.out_rows * k.mtiles;  // and every piece has a row
   const int pairs = (int)std::min<int64_t>(d.sms / 2, std::min(most, mine));
-  kernel<<<2 * pairs, kThreads, kSmemBytes, st>>>(map, xmap, k);
+  kernel<<<2 * pairs, kThreads, kSmemBytes, st>>>(map, xmaps, k);
   return cudaGetLastError() == cudaSuccess ? MSB_OK : MSB_ECUDA;
 }
 
 }  // namespace
 
 int launch_grouped(const GroupedArgs& a, cudaStream_t st) {
-  CUtensorMap map, xmap;
-  if (!weight_map(a, &map) || !rows_map(a, &xmap)) return MSB_ECUDA;
+  CUtensorMap map;
+  RowMaps xmaps = {};
+  if (!weight_map(a, &map) || !row_maps(a, &xmaps)) return MSB_ECUDA;
   const int es = a.i8 ? 1 : 2;
   KArgs k;
   k.x_rows = a.x_rows;
@@ -543,16 +579,16 @@ int launch_grouped(const GroupedArgs& a, cudaStream_t st) {
   k.ldo = a.ldo;
   k.wide = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && (a.ldo % 8 == 0 || a.out_rows == 1);
   if (a.i8) {
-    if (a.swiglu) return launch<true, false, true, false>(map, xmap, k, st);
-    return a.out_f32 ? launch<true, false, false, true>(map, xmap, k, st)
-                     : launch<true, false, false, false>(map, xmap, k, st);
+    if (a.swiglu) return launch<true, false, true, false>(map, xmaps, k, st);
+    return a.out_f32 ? launch<true, false, false, true>(map, xmaps, k, st)
+                     : launch<true, false, false, false>(map, xmaps, k, st);
   }
-  if (a.swiglu) return launch<false, false, true, false>(map, xmap, k, st);
+  if (a.swiglu) return launch<false, false, true, false>(map, xmaps, k, st);
   if (a.w_k != 1)
-    return a.out_f32 ? launch<false, true, false, true>(map, xmap, k, st)
-                     : launch<false, true, false, false>(map, xmap, k, st);
-  return a.out_f32 ? launch<false, false, false, true>(map, xmap, k, st)
-                   : launch<false, false, false, false>(map, xmap, k, st);
+    return a.out_f32 ? launch<false, true, false, true>(map, xmaps, k, st)
+                     : launch<false, true, false, false>(map, xmaps, k, st);
+  return a.out_f32 ? launch<false, false, false, true>(map, xmaps, k, st)
+                   : launch<false, false, false, false>(map, xmaps, k, st);
 }
 
 int dense_check(cudaStream_t st) {
