@@ -9,13 +9,16 @@
 // (a group of c rows is cut into ceil(c / 256) even pieces).  One row streams its experts'
 // weights; a prompt runs at the matrix unit's rate.
 //
-// One CTA pair per tile (persistent, static order), 10 warps a CTA:
+// One CTA pair per tile (persistent, static order), 12 warps a CTA:
 //   warps 0-3  epilogue: tensor memory -> registers -> scale / SwiGLU -> global
 //   warp 4     issues the matrix instructions (even CTA) into one of two accumulators
 //   warp 5     weights: one, two or eight tensor-map boxes per stage of 128 bytes of k
-//   warps 6-9  rows of x: boxes of 128, 64, 32 and 16 rows (warp 6), or gathered four rows to an
-//              instruction, an eighth of each warp's instructions at a time (one thread issues
-//              an instruction in about 60 cycles, and 128 rows take 32 of them)
+//   warps 6-11 rows of x.  In order: boxes of 128, 64, 32 and 16 rows (warp 6).  Gathered: each
+//              warp fills every sixth stage by 16-byte asynchronous copies in the same swizzle,
+//              waits for them and hands the stage over.  (The fence that makes copied bytes
+//              visible to the matrix unit waits for all copies of its thread, so a stage's
+//              copies are all that its warp has in flight; a gathering tensor-map load, four
+//              rows an instruction, takes the copy unit 60 to 80 cycles for 512 bytes.)
 #include <cuda.h>
 
 #include <algorithm>
@@ -37,8 +40,8 @@ constexpr int kStageBytes = 128;  // bytes of k per stage (one swizzle row)
 constexpr int kStages = 6;
 constexpr int kABytes = 128 * kStageBytes;           // one CTA's weight rows
 constexpr int kBBytes = kTileN / 2 * kStageBytes;    // one CTA's rows of x
-constexpr int kThreads = 320;
-constexpr int kNoRow = 0x7fffffff;  // a row index outside any x: the load fills zeros
+constexpr int kRowWarps = kStages;  // gathering warps
+constexpr int kThreads = (6 + kRowWarps) * 32;
 
 // Bytes between the staged rows of an epilogue warp's 32 bf16 channels: 64 and 16 more, so that
 // eight rows' 16-byte pieces fall into different banks.
@@ -51,12 +54,15 @@ struct Shared {
   int32_t first[kGroupsMax + 1];  // first piece of each group
   int32_t begin[kGroupsMax + 1];  // first row of each group
   float scale[4][kTileN];         // 8-bit: scales of the tile's rows of x, per epilogue warp
+  int32_t row[kRowWarps][kTileN / 2];  // gathering: a tile's rows of x, -1 for none
   alignas(16) uint8_t out[4][32 * kOutPitch];  // 32 rows of an epilogue warp's channels
 };
 constexpr size_t kSmemBytes = (size_t)kStages * (kABytes + kBBytes) + 1024 + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 struct KArgs {
+  const uint8_t* x;
+  int64_t pitch;  // bytes between rows of x
   int32_t x_rows;
   const int32_t* rows;
   const int32_t* offsets;
@@ -68,7 +74,7 @@ struct KArgs {
   int wide;  // out may be written in 16-byte pieces
 };
 
-// Tensor maps of x: boxes of 16 << i rows, or of one row (map 0) for the gathering load.
+// Tensor maps of x in order: boxes of 16 << i rows.
 struct RowMaps {
   CUtensorMap map[4];
 };
@@ -294,9 +300,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(&s.tmem, 512);
   } else if (warp == 5 && lane == 0) {
     prefetch_map(&wmap);
-    for (int i = 0; i < (a.rows ? 1 : 4); ++i) prefetch_map(&xmaps.map[i]);
+    for (int i = 0; i < 4 && !a.rows; ++i) prefetch_map(&xmaps.map[i]);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&s.full[i], 1);
+      mbar_init(&s.full[i], a.rows ? 3 : 1);
       mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -320,7 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     for (int t = pair; ok && t < tiles; t += pairs) {
       const Tile tile = tile_at(a, s, t);
-      const uint32_t bytes = 2 * kABytes + ((tile.rows + 31) & ~31) * kStageBytes;
+      const uint32_t bytes = 2 * kABytes + (a.rows ? 0 : ((tile.rows + 31) & ~31) * kStageBytes);
       for (int i = 0; i < nk; ++i) {
         if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
         const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
@@ -370,36 +376,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mma_commit_pair(&s.acc_full[buf]);
       if (++buf == 2) buf = 0, acc_phase ^= 1;
     }
-  } else if (warp >= 6 && a.rows && lane == 0) {
+  } else if (warp >= 6 && a.rows) {
     // ------------------------------------------------ rows of x, gathered
-    int st = 0;
+    const int st = warp - 6;
+    int32_t* const table = s.row[st];
+    const uint32_t base = smem_addr(stages) + st * (kABytes + kBBytes) + kABytes;
+    const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
+    const int chunk = lane & 7, r0 = lane >> 3;  // 16-byte piece, row of each four
     uint32_t phase = 0;
+    int at = 0;  // stages before this tile, modulo the ring
     for (int t = pair; ok && t < tiles; t += pairs) {
       const Tile tile = tile_at(a, s, t);
       const int half = ((tile.rows + 31) & ~31) >> 1;  // this CTA's rows of the tile
-      // this warp takes four rows of every 16
-      int4 row[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        row[q] = make_int4(kNoRow, kNoRow, kNoRow, kNoRow);
-        const int c = (int)rank * half + q * 16 + (warp - 6) * 4, left = tile.rows - c;
-        if (q * 16 < half) {
-          const int32_t* r = a.rows + tile.row0 + c;
-          if (left > 0 && (uint32_t)r[0] < (uint32_t)a.x_rows) row[q].x = r[0];
-          if (left > 1 && (uint32_t)r[1] < (uint32_t)a.x_rows) row[q].y = r[1];
-          if (left > 2 && (uint32_t)r[2] < (uint32_t)a.x_rows) row[q].z = r[2];
-          if (left > 3 && (uint32_t)r[3] < (uint32_t)a.x_rows) row[q].w = r[3];
-        }
+      int i = st - at;
+      if (i < 0) i += kStages;
+      at = (at + nk) % kStages;
+      if (i >= nk) continue;
+      __syncwarp();  // the last tile's table has been read
+      for (int c = lane; c < half; c += 32) {
+        const int p = (int)rank * half + c;
+        const int row = p < tile.rows ? a.rows[tile.row0 + p] : -1;
+        table[c] = (uint32_t)row < (uint32_t)a.x_rows ? row : -1;
       }
-      for (int i = 0; i < nk; ++i) {
-        if (!(ok = wait_one(&s.empty[st], phase ^ 1, &s.dead))) break;
-        const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
-        const uint32_t dst = smem_addr(stages) + st * (kABytes + kBBytes) + kABytes + (warp - 6) * 4 * kStageBytes;
-        const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (q * 16 < half) tma_gather4(dst + q * 16 * kStageBytes, &xmaps.map[0], k0, row[q], bar);
-        if (++st == kStages) st = 0, phase ^= 1;
+      __syncwarp();
+      for (; i < nk; i += kStages) {
+        if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
+        phase ^= 1;
+        const int left = a.kbytes - i * kStageBytes - chunk * 16;
+        const uint32_t valid = left < 0 ? 0 : left > 16 ? 16 : left;
+        const uint8_t* const src = a.x + (int64_t)i * kStageBytes + chunk * 16;
+#pragma unroll 8
+        for (int r = r0; r < half; r += 4) {
+          const int row = table[r];
+          const bool use = row >= 0 && valid != 0;
+          cp_async16(base + r * kStageBytes + ((chunk ^ (r & 7)) << 4),
+                     use ? src + (int64_t)row * a.pitch : a.x, use ? valid : 0);
+        }
+        cp_async_wait_all();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(bar);
       }
     }
   } else if (warp == 6 && !a.rows && lane == 0) {
@@ -516,13 +532,13 @@ bool weight_map(const GroupedArgs& a, CUtensorMap* map) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tensor maps of x: {k, row}, boxes of 128 bytes.
+// Tensor maps of x: {k, row}, boxes of 128 bytes (none when the rows are gathered).
 bool row_maps(const GroupedArgs& a, RowMaps* maps) {
   const int es = a.i8 ? 1 : 2;
   const cuuint64_t dims[2] = {(cuuint64_t)a.k, (cuuint64_t)std::max(a.x_rows, 1)};
   const cuuint64_t strides[1] = {(cuuint64_t)(a.x_rows > 1 ? a.ldx * es : (a.k * es + 15) / 16 * 16)};
-  for (int i = 0; i < (a.rows ? 1 : 4); ++i) {
-    const cuuint32_t box[2] = {(cuuint32_t)(kStageBytes / es), a.rows ? 1u : 16u << i}, ones[2] = {1, 1};
+  for (int i = 0; i < 4 && !a.rows; ++i) {
+    const cuuint32_t box[2] = {(cuuint32_t)(kStageBytes / es), 16u << i}, ones[2] = {1, 1};
     if (encode_fn()(&maps->map[i], a.i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                     const_cast<void*>(a.x), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -565,6 +581,8 @@ int launch_grouped(const GroupedArgs& a, cudaStream_t st) {
   if (!weight_map(a, &map) || !row_maps(a, &xmaps)) return MSB_ECUDA;
   const int es = a.i8 ? 1 : 2;
   KArgs k;
+  k.x = static_cast<const uint8_t*>(a.x);
+  k.pitch = a.ldx * es;
   k.x_rows = a.x_rows;
   k.rows = a.rows;
   k.offsets = a.offsets;

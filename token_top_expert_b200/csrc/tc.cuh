@@ -140,17 +140,17 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int c
       "l"(map), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
-// Four rows (one-row boxes) at column c0, 128 bytes each, to consecutive rows of `dst`.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* map, int c0, int4 row, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4"
-      ".mbarrier::complete_tx::bytes [%0], [%1, {%2,%3,%4,%5,%6}], [%7];" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(row.x), "r"(row.y), "r"(row.z), "r"(row.w), "r"(bar)
-      : "memory");
-}
-
 __device__ __forceinline__ void prefetch_map(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// 16 bytes global -> shared, the bytes past `valid` (0..16) zero-filled and not read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
