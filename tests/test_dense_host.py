@@ -43,7 +43,8 @@ def matmul(lib, st, w=None, fn="msb_grouped_matmul", **kw):
 
 BAD = [dict(x=None), dict(out=None), dict(x=B + 2), dict(groups=0), dict(out_rows=-1), dict(x_rows=-1),
        dict(n=0), dict(k=0), dict(offsets=None), dict(out_type=2), dict(ldo=63), dict(ldx=-8),
-       dict(ldx=1 << 28), dict(ldo=1 << 28), dict(ldx=132), dict(out=B + 64), dict(out=A + 128)]
+       dict(ldx=1 << 28), dict(ldo=1 << 28), dict(ldx=132), dict(out=B + 64), dict(out=A + 128),
+       dict(rows=A + 2), dict(offsets=A + 1), dict(out=2 * B + 1)]
 
 
 @pytest.mark.parametrize("kw", BAD, ids=str)
@@ -91,7 +92,8 @@ def test_route_refusals(lib, st):
     for kw in (dict(logits=None), dict(t=2), dict(ld=63), dict(ld=-1), dict(tokens=-1), dict(experts=0),
                dict(top_e=0), dict(top_e=65), dict(renorm=2), dict(ids=None), dict(weights=None),
                dict(offsets=None), dict(rows=None), dict(pos=None), dict(ws=None),
-               dict(nb=lib.msb_route_workspace_size(100, 64) - 1)):
+               dict(nb=lib.msb_route_workspace_size(100, 64) - 1), dict(logits=A + 1), dict(ids=B + 2),
+               dict(pos=B + 1)):
         assert call(**kw) == st.MSB_EINVAL, kw
     for kw in (dict(tokens=(1 << 20) + 1), dict(experts=513, ld=600), dict(top_e=17)):
         assert call(**kw) == st.MSB_EUNSUPPORTED, kw
@@ -105,7 +107,7 @@ def test_quantize_refusals(lib, st):
         v.update(kw)
         return lib.msb_int8_quantize(*v.values(), None)
     for kw in (dict(x=None), dict(t=3), dict(ldx=-1), dict(rows=-1), dict(k=0), dict(q=None), dict(ldq=99),
-               dict(scale=None), dict(q=A + 64), dict(scale=A + 64), dict(scale=B + 64)):
+               dict(scale=None), dict(q=A + 64), dict(scale=A + 64), dict(scale=B + 64), dict(x=A + 1), dict(scale=2 * B + 2)):
         assert call(**kw) == st.MSB_EINVAL, kw
     assert call(rows=0, x=None, q=None, scale=None) == st.MSB_OK
 
@@ -116,7 +118,8 @@ def test_combine_refusals(lib, st):
         v.update(kw)
         return lib.msb_combine(*v.values(), None)
     for kw in (dict(y=None), dict(t=-1), dict(ldy=-1), dict(yr=-1), dict(pos=None), dict(w=None),
-               dict(tokens=-1), dict(top_e=0), dict(d=0), dict(out=None), dict(ldo=127), dict(out=A + 256)):
+               dict(tokens=-1), dict(top_e=0), dict(d=0), dict(out=None), dict(ldo=127), dict(out=A + 256),
+               dict(pos=B + 2), dict(out=3 * B + 1)):
         assert call(**kw) == st.MSB_EINVAL, kw
     assert call(tokens=0, out=None, pos=None, w=None) == st.MSB_OK
 
@@ -132,6 +135,7 @@ def test_block_norm_refusals(lib, st):
                dict(eps=float("nan")), dict(rows=-1), dict(d=0), dict(ldh=-1), dict(ldho=127), dict(ldx=127),
                dict(gr=-1), dict(gc=-1), dict(ho=None, x=None), dict(y=None), dict(pn=0),
                dict(ho=A, ldho=256), dict(ho=A + 64), dict(x=A + 64), dict(x=2 * A + 64), dict(ho=2 * A),
+               dict(h=A + 2), dict(y=2 * A + 1), dict(gate=5 * A + 1), dict(pre=3 * A + 1), dict(x=7 * A + 1),
                dict(x=6 * A + 64), dict(x=5 * A), dict(ho=3 * A), dict(x=4 * A)):
         assert call(**kw) == st.MSB_EINVAL, kw
     assert call(d=st.MSB_NORM_MAX_D + 1, ldho=1 << 15, ldx=1 << 15) == st.MSB_EUNSUPPORTED

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "common.cuh"
 #include "dense.h"
@@ -14,7 +15,14 @@ namespace {
 
 constexpr int64_t kMaxStride = (int64_t)1 << 39;  // bytes between neighbours a tensor map takes
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+bool aligned16(const void* p) { return aligned(p, 16); }
+// Arrays of 4-byte elements (null ones pass).
+bool aligned4(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!aligned(p, 4)) return false;
+  return true;
+}
 bool type_ok(int32_t t) { return t == MSB_BF16 || t == MSB_F32; }
 int64_t size_of(int32_t t) { return t == MSB_F32 ? 4 : 2; }
 
@@ -39,6 +47,7 @@ int grouped(GroupedArgs a, const msb_group_weights* w, int32_t out_type, cudaStr
   if (!w->data || (a.i8 && !a.w_scale) || (a.out_rows > 0 && (!a.x || !a.out || (a.i8 && !a.x_scale))))
     return MSB_EINVAL;
   if (!aligned16(a.x) || !aligned16(w->data) || !pitch_ok(a.ldx) || !pitch_ok(a.ldo)) return MSB_EINVAL;
+  if (!aligned4({a.rows, a.offsets, a.x_scale, a.w_scale}) || !aligned(a.out, size_of(out_type))) return MSB_EINVAL;
   if (a.x_rows > 1 && (a.ldx < 1 || a.ldx * es % 16)) return MSB_EINVAL;
   if (a.out_rows > 1 && a.ldo < a.n) return MSB_EINVAL;
   if (!a.rows && a.x_rows < a.out_rows) return MSB_EINVAL;
@@ -137,6 +146,7 @@ int dense_block(const void* x, int32_t tokens, const uint8_t* mask, const void* 
   if (tokens > MSB_DENSE_MAX_TOKENS) return MSB_EUNSUPPORTED;
   if (!x || !router_t || !w.gate_up || !w.down || !out || !workspace) return MSB_EINVAL;
   if (w.int8 && (!w.gate_up_scale || !w.down_scale)) return MSB_EINVAL;
+  if (!aligned4({w.gate_up_scale, w.down_scale}) || !aligned(out, 2)) return MSB_EINVAL;
   if (!aligned16(x) || !aligned16(router_t) || !aligned16(w.gate_up) || !aligned16(w.down) ||
       !aligned16(workspace))
     return MSB_EINVAL;
@@ -218,6 +228,8 @@ int32_t msb_route(const void* logits, int32_t logits_type, int64_t ld, const uin
     return MSB_EUNSUPPORTED;
   if (!offsets || !workspace || (tokens > 0 && (!logits || !ids || !weights || !rows || !pos)))
     return MSB_EINVAL;
+  if (!aligned4({ids, weights, offsets, rows, pos, workspace}) || !aligned(logits, size_of(logits_type)))
+    return MSB_EINVAL;
   if (workspace_bytes < msb_route_workspace_size(tokens, experts)) return MSB_EINVAL;
   return launch_route(logits, logits_type == MSB_BF16, ld, mask, tokens, experts, top_e, renorm != 0,
                       ids, weights, offsets, rows, pos, static_cast<int32_t*>(workspace),
@@ -246,6 +258,7 @@ int32_t msb_int8_quantize(const void* x, int32_t x_type, int64_t ldx, int32_t ro
   if (rows < 0 || k < 1 || !type_ok(x_type) || !pitch_ok(ldx) || !pitch_ok(ldq) ||
       (rows > 1 && ldq < k) || (rows > 0 && (!x || !q || !scale)))
     return MSB_EINVAL;
+  if (!aligned(x, size_of(x_type)) || !aligned(scale, 4)) return MSB_EINVAL;
   if (overlaps(x, extent(rows, ldx, k, size_of(x_type)), q, extent(rows, ldq, k, 1)) ||
       overlaps(scale, 4 * (int64_t)rows, q, extent(rows, ldq, k, 1)) ||
       overlaps(scale, 4 * (int64_t)rows, x, extent(rows, ldx, k, size_of(x_type))))
@@ -281,6 +294,7 @@ int32_t msb_combine(const void* y, int32_t y_type, int64_t ldy, int32_t y_rows, 
       !pitch_ok(ldo) || (tokens > 1 && ldo < d))
     return MSB_EINVAL;
   if (tokens > 0 && (!pos || !weights || !out || (y_rows > 0 && !y))) return MSB_EINVAL;
+  if (!aligned4({pos, weights}) || !aligned(y, size_of(y_type)) || !aligned(out, 2)) return MSB_EINVAL;
   if (overlaps(y, extent(y_rows, ldy, d, size_of(y_type)), out, extent(tokens, ldo, d, 2)))
     return MSB_EINVAL;
   if (tokens == 0) return MSB_OK;
@@ -302,6 +316,10 @@ int32_t msb_block_norm(const void* h, int32_t h_type, int64_t ldh, const void* y
   if (d > MSB_NORM_MAX_D) return MSB_EUNSUPPORTED;
   if ((!h_out && !x) || (rows > 0 && !h)) return MSB_EINVAL;
   if (!y && (gate || post_norm || post_weight)) return MSB_EINVAL;
+  if (!aligned(h, size_of(h_type)) || !aligned(h_out, size_of(h_type)) || !aligned(x, 2) ||
+      (y && !aligned(y, size_of(y_type))) || (gate && !aligned(gate, size_of(gate_type))) ||
+      !aligned(pre_weight, size_of(weight_type)) || !aligned(post_weight, size_of(weight_type)))
+    return MSB_EINVAL;
   if (post_weight && !post_norm) return MSB_EINVAL;
   if (!pitch_ok(ldh) || !pitch_ok(ldy) || !pitch_ok(ldh_out) || !pitch_ok(ldx) || !pitch_ok(gate_row) ||
       !pitch_ok(gate_col) || (rows > 1 && ((h_out && ldh_out < d) || (x && ldx < d))))
