@@ -22,6 +22,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cstddef>
 #include <mutex>
 
 #include "grouped.h"
@@ -53,10 +54,12 @@ struct Shared {
   uint32_t tmem, dead;
   int32_t first[kGroupsMax + 1];  // first piece of each group
   int32_t begin[kGroupsMax + 1];  // first row of each group
-  float scale[4][kTileN];         // 8-bit: scales of the tile's rows of x, per epilogue warp
+  alignas(16) float scale[4][kTileN];  // 8-bit: scales of the tile's rows of x, per epilogue warp
   int32_t row[kRowWarps][kTileN / 2];  // gathering: a tile's rows of x, -1 for none
   alignas(16) uint8_t out[4][32 * kOutPitch];  // 32 rows of an epilogue warp's channels
 };
+static_assert(offsetof(Shared, scale) % 16 == 0 && offsetof(Shared, out) % 16 == 0 && kOutPitch % 16 == 0,
+              "vector accesses");
 constexpr size_t kSmemBytes = (size_t)kStages * (kABytes + kBBytes) + 1024 + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
