@@ -9,15 +9,15 @@
 // (a group of c rows is cut into ceil(c / 256) even pieces).  One row streams its experts'
 // weights; a prompt runs at the matrix unit's rate.
 //
-// One CTA pair per tile (persistent, static order), 12 warps a CTA:
+// One CTA pair per tile (persistent, static order), 18 warps a CTA:
 //   warps 0-3  epilogue: tensor memory -> registers -> scale / SwiGLU -> global
 //   warp 4     issues the matrix instructions (even CTA) into one of two accumulators
 //   warp 5     weights: one, two or eight tensor-map boxes per stage of 128 bytes of k
-//   warps 6-11 rows of x.  In order: boxes of 128, 64, 32 and 16 rows (warp 6).  Gathered: each
-//              warp fills every sixth stage by 16-byte asynchronous copies in the same swizzle,
-//              waits for them and hands the stage over.  (The fence that makes copied bytes
+//   warps 6-17 rows of x.  In order: boxes of 128, 64, 32 and 16 rows (warp 6).  Gathered: two
+//              warps to a stage copy 16 bytes a thread, asynchronously, into the same swizzle,
+//              wait for them and hand the stage over.  (The fence that makes copied bytes
 //              visible to the matrix unit waits for all copies of its thread, so a stage's
-//              copies are all that its warp has in flight; a gathering tensor-map load, four
+//              copies are all that its warps have in flight; a gathering tensor-map load, four
 //              rows an instruction, takes the copy unit 60 to 80 cycles for 512 bytes.)
 #include <cuda.h>
 
@@ -41,7 +41,9 @@ constexpr int kStageBytes = 128;  // bytes of k per stage (one swizzle row)
 constexpr int kStages = 6;
 constexpr int kABytes = 128 * kStageBytes;           // one CTA's weight rows
 constexpr int kBBytes = kTileN / 2 * kStageBytes;    // one CTA's rows of x
-constexpr int kRowWarps = kStages;  // gathering warps
+constexpr int kSplit = 2;                    // gathering warps of a stage
+constexpr int kRowWarps = kSplit * kStages;
+constexpr int kLaneRows = kTileN / 2 / kSplit / 4;  // rows of a gathering thread
 constexpr int kThreads = (6 + kRowWarps) * 32;
 
 // Bytes between the staged rows of an epilogue warp's 32 bf16 channels: 64 and 16 more, so that
@@ -55,7 +57,6 @@ struct Shared {
   int32_t first[kGroupsMax + 1];  // first piece of each group
   int32_t begin[kGroupsMax + 1];  // first row of each group
   alignas(16) float scale[4][kTileN];  // 8-bit: scales of the tile's rows of x, per epilogue warp
-  int32_t row[kRowWarps][kTileN / 2];  // gathering: a tile's rows of x, -1 for none
   alignas(16) uint8_t out[4][32 * kOutPitch];  // 32 rows of an epilogue warp's channels
 };
 static_assert(offsetof(Shared, scale) % 16 == 0 && offsetof(Shared, out) % 16 == 0 && kOutPitch % 16 == 0,
@@ -177,6 +178,13 @@ __device__ __forceinline__ float value(uint32_t v, float row_scale, float scale)
   return __uint_as_float(v);
 }
 
+// This warp has read all it wants of an accumulator.
+__device__ __forceinline__ void release_acc(Shared& s, int buf, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) arrive_pair(map_to(smem_addr(&s.acc_empty[buf]), 0));
+}
+
 // One epilogue warp's 32 channels of the accumulator to float: a lane is a channel.
 template <bool I8>
 __device__ __forceinline__ bool store_f32(const KArgs& a, Shared& s, const Tile& tile, uint32_t tmem, int buf,
@@ -189,6 +197,7 @@ __device__ __forceinline__ bool store_f32(const KArgs& a, Shared& s, const Tile&
     uint32_t v[32];
     tmem_ld32(tmem + buf * kTileN + ((uint32_t)(warp * 32) << 16) + c0, v);
     tmem_ld_wait();
+    if (c0 + 32 >= tile.rows) release_acc(s, buf, lane);
     if (ch < a.n) {
       float* const out = static_cast<float*>(a.out) + (int64_t)(tile.row0 + c0) * a.ldo + ch;
 #pragma unroll
@@ -229,6 +238,7 @@ __device__ __forceinline__ bool store_bf16(const KArgs& a, Shared& s, const Tile
     tmem_ld16(acc + c0, v[0]);
     tmem_ld16(acc + (16u << 16) + c0, v[1]);
     tmem_ld_wait();
+    if (c0 + 32 >= tile.rows) release_acc(s, buf, lane);
     __syncwarp();  // the last 32 rows have been read
     float2 rs[4];
 #pragma unroll
@@ -305,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_map(&wmap);
     for (int i = 0; i < 4 && !a.rows; ++i) prefetch_map(&xmaps.map[i]);
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&s.full[i], a.rows ? 3 : 1);
+      mbar_init(&s.full[i], a.rows ? 1 + 2 * kSplit : 1);
       mbar_init(&s.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -381,44 +391,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 6 && a.rows) {
     // ------------------------------------------------ rows of x, gathered
-    const int st = warp - 6;
-    int32_t* const table = s.row[st];
-    const uint32_t base = smem_addr(stages) + st * (kABytes + kBBytes) + kABytes;
+    const int st = (warp - 6) / kSplit, part = (warp - 6) % kSplit;
+    const int chunk = lane & 7, r0 = lane >> 3;  // 16-byte piece of 128, row of each four
     const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
-    const int chunk = lane & 7, r0 = lane >> 3;  // 16-byte piece, row of each four
+    const uint32_t base = smem_addr(stages) + st * (kABytes + kBBytes) + kABytes + r0 * kStageBytes;
     uint32_t phase = 0;
     int at = 0;  // stages before this tile, modulo the ring
     for (int t = pair; ok && t < tiles; t += pairs) {
       const Tile tile = tile_at(a, s, t);
       const int half = ((tile.rows + 31) & ~31) >> 1;  // this CTA's rows of the tile
+      const int mine = half / kSplit;  // this warp's: 8, 16, .. kLaneRows * 4 from part * mine on
       int i = st - at;
       if (i < 0) i += kStages;
       at = (at + nk) % kStages;
       if (i >= nk) continue;
-      __syncwarp();  // the last tile's table has been read
-      for (int c = lane; c < half; c += 32) {
-        const int p = (int)rank * half + c;
-        const int row = p < tile.rows ? a.rows[tile.row0 + p] : -1;
-        table[c] = (uint32_t)row < (uint32_t)a.x_rows ? row : -1;
+      const uint8_t* src[kLaneRows];
+      uint32_t there = 0;  // rows that exist
+#pragma unroll
+      for (int q = 0; q < kLaneRows; ++q) {
+        const int p = (int)rank * half + part * mine + q * 4 + r0;
+        const int row = q * 4 < mine && p < tile.rows ? a.rows[tile.row0 + p] : -1;
+        const bool use = (uint32_t)row < (uint32_t)a.x_rows;
+        there |= (uint32_t)use << q;
+        src[q] = a.x + (use ? (int64_t)row * a.pitch + chunk * 16 : 0);
       }
-      __syncwarp();
       for (; i < nk; i += kStages) {
         if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
         phase ^= 1;
         const int left = a.kbytes - i * kStageBytes - chunk * 16;
         const uint32_t valid = left < 0 ? 0 : left > 16 ? 16 : left;
-        const uint8_t* const src = a.x + (int64_t)i * kStageBytes + chunk * 16;
-#pragma unroll 8
-        for (int r = r0; r < half; r += 4) {
-          const int row = table[r];
-          const bool use = row >= 0 && valid != 0;
-          cp_async16(base + r * kStageBytes + ((chunk ^ (r & 7)) << 4),
-                     use ? src + (int64_t)row * a.pitch : a.x, use ? valid : 0);
-        }
+        const int64_t k0 = valid ? (int64_t)i * kStageBytes : 0;
+#pragma unroll
+        for (int q = 0; q < kLaneRows; ++q)
+          if (q * 4 < mine)
+            cp_async16(base + (part * mine + q * 4) * kStageBytes + ((chunk ^ ((q * 4 + r0) & 7)) << 4),
+                       src[q] + (there >> q & 1 ? k0 : 0), there >> q & 1 ? valid : 0);
         cp_async_wait_all();
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) arrive_cluster(bar);
+        if (lane == 0) arrive_pair(bar);
       }
     }
   } else if (warp == 6 && !a.rows && lane == 0) {
@@ -459,14 +470,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+      // the accumulator is handed back once it has been read, before the last stores
       if constexpr (F32)
         ok = store_f32<I8>(a, s, tile, tmem, buf, acc_phase, rank, warp, lane);
       else
         ok = store_bf16<I8, GATED>(a, s, tile, tmem, buf, acc_phase, rank, warp, lane);
-      if (!ok) break;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(map_to(smem_addr(&s.acc_empty[buf]), 0));
       if (++buf == 2) buf = 0, acc_phase ^= 1;
     }
   }

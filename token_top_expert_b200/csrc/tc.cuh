@@ -164,8 +164,12 @@ __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrive on a barrier of either CTA, with the default release at CTA scope.  It hands over
+// shared memory of the arriving CTA itself or tensor memory, both complete and fenced for the
+// matrix unit before; only the signal crosses the pair.  (A release at cluster scope would
+// also wait for the thread's stores to global memory: about 2100 cycles here.)
+__device__ __forceinline__ void arrive_pair(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
