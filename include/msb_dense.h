@@ -11,7 +11,7 @@
  *   msb_grouped_matmul   products of ragged groups of rows with their group's weight
  *   msb_grouped_swiglu   the same for gate and up, with SwiGLU
  *   msb_int8_quantize    rows to 8-bit integers with one scale each
- *   msb_int8_matmul, msb_int8_swiglu   the products in 8-bit integers
+ *   msb_int8_matmul, msb_int8_swiglu, msb_int8_linear   the products in 8-bit integers
  *   msb_combine          a token's expert rows summed by router weight
  *   msb_block_norm       norms before and after a block with its gate and residual scale
  *   moe_dense_block, moe_dense_block_int8   the whole block
@@ -131,6 +131,16 @@ int32_t msb_int8_swiglu(const int8_t* q, int64_t ldq, const float* q_scale, int3
                         const int32_t* rows, const int32_t* offsets, int32_t groups,
                         int32_t out_rows, const msb_group_weights* w, const float* w_scale,
                         int32_t n, int32_t k, void* out, int64_t ldo, void* stream);
+
+/* msb_int8_quantize of x, then msb_int8_matmul (swiglu = 0) or msb_int8_swiglu (swiglu = 1,
+ * out_type MSB_BF16): the same results.  workspace: msb_int8_linear_workspace_size(x_rows, k)
+ * bytes (at least 16; 0 for sizes out of range), 16-byte aligned, no initial contents needed. */
+size_t msb_int8_linear_workspace_size(int32_t x_rows, int32_t k);
+int32_t msb_int8_linear(const void* x, int32_t x_type, int64_t ldx, int32_t x_rows,
+                        const int32_t* rows, const int32_t* offsets, int32_t groups,
+                        int32_t out_rows, const msb_group_weights* w, const float* w_scale,
+                        int32_t n, int32_t k, int32_t swiglu, void* out, int32_t out_type,
+                        int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------ combine
  * out[t] = sum over k of weights[t][k] * y[pos[t][k]], in the order of k, in FP32, rounded

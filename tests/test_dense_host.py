@@ -112,6 +112,38 @@ def test_quantize_refusals(lib, st):
     assert call(rows=0, x=None, q=None, scale=None) == st.MSB_OK
 
 
+def test_int8_linear_refusals(lib, st):
+    nb = lib.msb_int8_linear_workspace_size(10, 100)
+    assert nb == 10 * (112 + 4)
+    assert lib.msb_int8_linear_workspace_size(0, 1) == 16
+    assert lib.msb_int8_linear_workspace_size(-1, 8) == lib.msb_int8_linear_workspace_size(1, 0) == 0
+    assert lib.msb_int8_linear_workspace_size(1, st.MSB_INT8_MAX_K + 1) == 0
+
+    def call(w=None, **kw):
+        v = dict(x=B, xt=0, ldx=100, xr=10, rows=None, offsets=None, groups=1, r=10)
+        u = dict(ws=A, n=64, k=100, swiglu=0, out=2 * B, ot=0, ldo=64, work=3 * B, nb=nb)
+        for k, val in kw.items():
+            (v if k in v else u)[k] = val
+        w = w or weights(st, stride_n=112)
+        return lib.msb_int8_linear(*v.values(), ctypes.byref(w), *u.values(), None)
+    for kw in (dict(x=None), dict(xt=2), dict(ldx=-1), dict(xr=-1), dict(k=0), dict(swiglu=2), dict(work=None),
+               dict(work=3 * B + 8), dict(nb=nb - 1), dict(x=B + 1), dict(work=B + 64), dict(out=B + 64),
+               dict(out=3 * B + 64), dict(ws=None), dict(n=0), dict(swiglu=1, ot=1), dict(r=11)):
+        assert call(**kw) == st.MSB_EINVAL, kw
+    assert call(k=st.MSB_INT8_MAX_K + 1) == st.MSB_EUNSUPPORTED
+    assert call(weights(st, stride_n=1, stride_k=64)) == st.MSB_EUNSUPPORTED
+
+
+def test_header_is_plain_c(tmp_path):
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "h.c"
+    src.write_text('#include "msb_dense.h"\nint main(void) { msb_group_weights w = {0, 0, 0, 0, 1}; return (int)w.stride_k - 1; }\n')
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-pedantic", "-fsyntax-only",
+                    "-I", os.path.join(root, "include"), str(src)], check=True)
+
+
 def test_combine_refusals(lib, st):
     def call(**kw):
         v = dict(y=A, t=0, ldy=128, yr=20, pos=B, w=2 * B, tokens=5, top_e=4, d=128, out=3 * B, ldo=128)

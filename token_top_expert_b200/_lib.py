@@ -40,6 +40,7 @@ SYMBOLS = (
     "msb_q4_record_bytes", "msb_pack_q4", "moe_sparse_block_q4",
     "msb_dense_check", "msb_route_workspace_size", "msb_route", "msb_grouped_matmul",
     "msb_grouped_swiglu", "msb_int8_quantize", "msb_int8_matmul", "msb_int8_swiglu",
+    "msb_int8_linear_workspace_size", "msb_int8_linear",
     "msb_combine", "msb_block_norm", "msb_dense_workspace_size", "moe_dense_block",
     "moe_dense_block_int8",
 )
@@ -124,6 +125,8 @@ def load() -> ctypes.CDLL:
         "msb_int8_quantize": (I32, [P, I32, I64, I32, I32, P, I64, P, P]),
         "msb_int8_matmul": (I32, [P, I64, P, I32, P, P, I32, I32, w_p, P, I32, I32, P, I32, I64, P]),
         "msb_int8_swiglu": (I32, [P, I64, P, I32, P, P, I32, I32, w_p, P, I32, I32, P, I64, P]),
+        "msb_int8_linear_workspace_size": (SZ, [I32, I32]),
+        "msb_int8_linear": (I32, [P, I32, I64, I32, P, P, I32, I32, w_p, P, I32, I32, I32, P, I32, I64, P, SZ, P]),
         "msb_combine": (I32, [P, I32, I64, I32, P, P, I32, I32, I32, P, I64, P]),
         "msb_block_norm": (I32, [P, I32, I64, P, I32, I64, P, P, I32, I32, P, I32, I64, I64, F32, F32,
                                  F32, P, I64, P, I64, I32, I32, P]),

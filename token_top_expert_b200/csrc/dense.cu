@@ -38,7 +38,9 @@ bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
 // A row pitch in elements that the byte arithmetic of a call can take (2^31 rows, 4 bytes).
 bool pitch_ok(int64_t ld) { return ld >= 0 && ld < (int64_t)1 << 28; }
 
-int grouped(GroupedArgs a, const msb_group_weights* w, int32_t out_type, cudaStream_t st) {
+// Checks the arguments of a grouped product and completes `a`; MSB_OK with a.out_rows = 0 means
+// that there is nothing to do.
+int grouped_check(GroupedArgs& a, const msb_group_weights* w, int32_t out_type) {
   const int64_t es = a.i8 ? 1 : 2;
   if (!w || a.groups < 1 || a.n < 1 || a.k < 1 || a.out_rows < 0 || a.x_rows < 0 || !type_ok(out_type))
     return MSB_EINVAL;
@@ -73,9 +75,13 @@ int grouped(GroupedArgs a, const msb_group_weights* w, int32_t out_type, cudaStr
   if (overlaps(a.out, out_bytes, a.x, extent(a.x_rows, a.ldx, a.k, es)) ||
       overlaps(a.out, out_bytes, a.w, w_bytes))
     return MSB_EINVAL;
-  if (a.out_rows == 0) return MSB_OK;
   a.out_f32 = out_type == MSB_F32;
-  return launch_grouped(a, st);
+  return MSB_OK;
+}
+
+int grouped(GroupedArgs a, const msb_group_weights* w, int32_t out_type, cudaStream_t st) {
+  const int rc = grouped_check(a, w, out_type);
+  return rc != MSB_OK || a.out_rows == 0 ? rc : launch_grouped(a, st);
 }
 
 GroupedArgs grouped_args(const void* x, int64_t ldx, int32_t x_rows, const int32_t* rows,
@@ -144,6 +150,7 @@ int dense_block(const void* x, int32_t tokens, const uint8_t* mask, const void* 
   if (!dense_dims_ok(dims, &rc)) return rc;
   if (tokens < 0) return MSB_EINVAL;
   if (tokens > MSB_DENSE_MAX_TOKENS) return MSB_EUNSUPPORTED;
+  if (tokens == 0) return MSB_OK;
   if (!x || !router_t || !w.gate_up || !w.down || !out || !workspace) return MSB_EINVAL;
   if (w.int8 && (!w.gate_up_scale || !w.down_scale)) return MSB_EINVAL;
   if (!aligned4({w.gate_up_scale, w.down_scale}) || !aligned(out, 2)) return MSB_EINVAL;
@@ -157,7 +164,6 @@ int dense_block(const void* x, int32_t tokens, const uint8_t* mask, const void* 
   if (overlaps(x, act, out, act) || overlaps(workspace, (int64_t)L.total, out, act) ||
       overlaps(workspace, (int64_t)L.total, x, act))
     return MSB_EINVAL;
-  if (tokens == 0) return MSB_OK;
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   const auto i32 = [ws](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
   const auto f32 = [ws](size_t at) { return reinterpret_cast<float*>(ws + at); };
@@ -287,6 +293,36 @@ int32_t msb_int8_swiglu(const int8_t* q, int64_t ldq, const float* q_scale, int3
   return grouped(a, w, MSB_BF16, static_cast<cudaStream_t>(stream));
 }
 
+size_t msb_int8_linear_workspace_size(int32_t x_rows, int32_t k) {
+  if (x_rows < 0 || k < 1 || k > MSB_INT8_MAX_K) return 0;
+  const size_t pitch = ((size_t)k + 15) & ~(size_t)15;
+  return std::max<size_t>((size_t)x_rows * (pitch + 4), 16);
+}
+
+int32_t msb_int8_linear(const void* x, int32_t x_type, int64_t ldx, int32_t x_rows,
+                        const int32_t* rows, const int32_t* offsets, int32_t groups,
+                        int32_t out_rows, const msb_group_weights* w, const float* w_scale,
+                        int32_t n, int32_t k, int32_t swiglu, void* out, int32_t out_type,
+                        int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
+  if (x_rows < 0 || k < 1 || !type_ok(x_type) || !pitch_ok(ldx) || (swiglu != 0 && swiglu != 1) ||
+      (swiglu && out_type != MSB_BF16) || !workspace || !aligned16(workspace) || !aligned(x, size_of(x_type)) ||
+      (x_rows > 0 && !x))
+    return MSB_EINVAL;
+  if (k > MSB_INT8_MAX_K) return MSB_EUNSUPPORTED;
+  const int64_t need = (int64_t)msb_int8_linear_workspace_size(x_rows, k), pitch = ((int64_t)k + 15) & ~15;
+  const int64_t xb = extent(x_rows, ldx, k, size_of(x_type)), ob = extent(out_rows, ldo, n, size_of(out_type));
+  if (workspace_bytes < (size_t)need || overlaps(workspace, need, x, xb) || overlaps(out, ob, x, xb)) return MSB_EINVAL;
+  int8_t* const q = static_cast<int8_t*>(workspace);
+  float* const scale = reinterpret_cast<float*>(q + x_rows * pitch);
+  GroupedArgs a = grouped_args(q, pitch, x_rows, rows, offsets, groups, out_rows, n, k, out, ldo);
+  a.i8 = true, a.swiglu = swiglu != 0, a.x_scale = scale, a.w_scale = w_scale;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int rc = grouped_check(a, w, out_type);
+  if (rc != MSB_OK || out_rows == 0) return rc;
+  if (x_rows > 0) rc = launch_quantize(x, x_type == MSB_F32, ldx, x_rows, k, q, pitch, scale, st);
+  return rc != MSB_OK ? rc : launch_grouped(a, st);
+}
+
 int32_t msb_combine(const void* y, int32_t y_type, int64_t ldy, int32_t y_rows, const int32_t* pos,
                     const float* weights, int32_t tokens, int32_t top_e, int32_t d, void* out,
                     int64_t ldo, void* stream) {
@@ -314,7 +350,8 @@ int32_t msb_block_norm(const void* h, int32_t h_type, int64_t ldh, const void* y
       ((pre_weight || post_weight) && !type_ok(weight_type)))
     return MSB_EINVAL;
   if (d > MSB_NORM_MAX_D) return MSB_EUNSUPPORTED;
-  if ((!h_out && !x) || (rows > 0 && !h)) return MSB_EINVAL;
+  if (rows == 0) return MSB_OK;
+  if ((!h_out && !x) || !h) return MSB_EINVAL;
   if (!y && (gate || post_norm || post_weight)) return MSB_EINVAL;
   if (!aligned(h, size_of(h_type)) || !aligned(h_out, size_of(h_type)) || !aligned(x, 2) ||
       (y && !aligned(y, size_of(y_type))) || (gate && !aligned(gate, size_of(gate_type))) ||
@@ -338,15 +375,14 @@ int32_t msb_block_norm(const void* h, int32_t h_type, int64_t ldh, const void* y
     if (overlaps(outs[i], sizes[i], y, yb) || overlaps(outs[i], sizes[i], gate, gb) ||
         overlaps(outs[i], sizes[i], pre_weight, wb) || overlaps(outs[i], sizes[i], post_weight, wb))
       return MSB_EINVAL;
-  if (rows == 0) return MSB_OK;
   NormArgs a;
   a.h = h, a.y = y, a.pre = pre_weight, a.post = post_weight, a.gate = gate, a.h_out = h_out;
   a.x = static_cast<uint16_t*>(x);
   a.ldh = ldh, a.ldy = ldy, a.ldh_out = ldh_out, a.ldx = ldx, a.gate_row = gate_row, a.gate_col = gate_col;
-  a.d = d, a.h_f32 = h_type == MSB_F32, a.y_f32 = y_type == MSB_F32, a.w_f32 = weight_type == MSB_F32;
+  a.rows = rows, a.d = d, a.h_f32 = h_type == MSB_F32, a.y_f32 = y_type == MSB_F32, a.w_f32 = weight_type == MSB_F32;
   a.gate_f32 = gate_type == MSB_F32, a.post_norm = post_norm != 0;
   a.skip = skip_scale, a.residual = residual_scale, a.eps = eps;
-  return launch_block_norm(a, rows, static_cast<cudaStream_t>(stream));
+  return launch_block_norm(a, static_cast<cudaStream_t>(stream));
 }
 
 size_t msb_dense_workspace_size(const msb_dims* dims, int32_t tokens, int32_t int8) {

@@ -8,6 +8,23 @@
 
 namespace msb {
 
+// Launch that may start while the kernel before it on the stream finishes; every kernel
+// launched so waits for that (griddepcontrol.wait) before it touches memory.
+template <typename... P, typename... A>
+int launch_early(void (*kernel)(P...), int64_t blocks, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? MSB_OK : MSB_ECUDA;
+}
+
 int route_blocks(int tokens);  // blocks of the routing kernels: rows of their histogram
 int launch_route(const void* logits, bool bf16, int64_t ld, const uint8_t* mask, int tokens,
                  int experts, int top_e, bool renorm, int32_t* ids, float* weights,
@@ -25,10 +42,10 @@ struct NormArgs {
   void* h_out;
   uint16_t* x;
   int64_t ldh, ldy, ldh_out, ldx, gate_row, gate_col;
-  int d;
+  int rows, d;
   bool h_f32, y_f32, w_f32, gate_f32, post_norm;
   float skip, residual, eps;
 };
-int launch_block_norm(const NormArgs& a, int rows, cudaStream_t st);
+int launch_block_norm(const NormArgs& a, cudaStream_t st);
 
 }  // namespace msb

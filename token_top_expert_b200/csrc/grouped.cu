@@ -25,6 +25,7 @@
 #include <cstddef>
 #include <mutex>
 
+#include "dense.h"
 #include "grouped.h"
 #include "tc.cuh"
 
@@ -307,7 +308,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int nk = (a.kbytes + kStageBytes - 1) / kStageBytes;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     plan_groups(a, s, lane);
   } else if (warp == 4) {
     tmem_alloc_pair(&s.tmem, 512);
@@ -325,6 +328,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     s.dead = 0;
     fence_mbar_init();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -580,8 +584,7 @@ int launch(const CUtensorMap& map, const RowMaps& xmaps, const KArgs& k, cudaStr
   const int64_t most = ((int64_t)k.groups + k.out_rows / kTileN) * k.mtiles;
   const int64_t mine = (int64_t)k.out_rows * k.mtiles;  // and every piece has a row
   const int pairs = (int)std::min<int64_t>(d.sms / 2, std::min(most, mine));
-  kernel<<<2 * pairs, kThreads, kSmemBytes, st>>>(map, xmaps, k);
-  return cudaGetLastError() == cudaSuccess ? MSB_OK : MSB_ECUDA;
+  return launch_early(kernel, 2 * pairs, kThreads, kSmemBytes, st, map, xmaps, k);
 }
 
 }  // namespace

@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kNT, 1)
   __shared__ PlaceShared s;
   __shared__ int32_t count[kMaxE];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int e = tid; e < experts; e += kNT) count[e] = 0;
   __syncthreads();
@@ -191,6 +192,7 @@ __global__ void __launch_bounds__(kNT, 1)
     place_kernel(const int32_t* ids, int32_t* rows, int32_t* pos, int32_t* offsets,
                  const int32_t* hist, int tokens, int experts, int top_e, int per) {
   __shared__ PlaceShared s;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   place(ids, rows, pos, offsets, hist, tokens, experts, top_e, per, s);
 }
@@ -205,20 +207,16 @@ int launch_route(const void* logits, bool bf16, int64_t ld, const uint8_t* mask,
                  int experts, int top_e, bool renorm, int32_t* ids, float* weights,
                  int32_t* offsets, int32_t* rows, int32_t* pos, int32_t* hist, cudaStream_t st) {
   const int nb = route_blocks(tokens), per = (tokens + nb - 1) / nb;
-#define MSB_ROUTE(NV)                                                                          \
-  (bf16 ? route_kernel<NV, true><<<nb, kNT, 0, st>>>(logits, ld, mask, tokens, experts, top_e, \
-                                                     renorm, ids, weights, offsets, rows, pos, \
-                                                     hist, per)                                \
-        : route_kernel<NV, false><<<nb, kNT, 0, st>>>(logits, ld, mask, tokens, experts,       \
-                                                      top_e, renorm, ids, weights, offsets,    \
-                                                      rows, pos, hist, per))
-  if (experts <= 64) MSB_ROUTE(2);
-  else if (experts <= 128) MSB_ROUTE(4);
-  else if (experts <= 256) MSB_ROUTE(8);
-  else MSB_ROUTE(16);
+#define MSB_ROUTE(NV)                                                                               \
+  launch_early(bf16 ? route_kernel<NV, true> : route_kernel<NV, false>, nb, kNT, 0, st, logits, ld, mask, \
+               tokens, experts, top_e, renorm ? 1 : 0, ids, weights, offsets, rows, pos, hist, per)
+  const int rc = experts <= 64    ? MSB_ROUTE(2)
+                 : experts <= 128 ? MSB_ROUTE(4)
+                 : experts <= 256 ? MSB_ROUTE(8)
+                                  : MSB_ROUTE(16);
 #undef MSB_ROUTE
-  if (nb > 1) place_kernel<<<nb, kNT, 0, st>>>(ids, rows, pos, offsets, hist, tokens, experts, top_e, per);
-  return cudaGetLastError() == cudaSuccess ? MSB_OK : MSB_ECUDA;
+  if (rc != MSB_OK || nb == 1) return rc;
+  return launch_early(place_kernel, nb, kNT, 0, st, ids, rows, pos, offsets, hist, tokens, experts, top_e, per);
 }
 
 }  // namespace msb

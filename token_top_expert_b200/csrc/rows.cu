@@ -1,129 +1,333 @@
 // Row-wise operators of the dense block: 8-bit quantisation, the weighted sum of a token's
-// expert rows, and the norms around a block.  All are bound by memory: one block per row.
+// expert rows, and the norms around a block.  All are bound by memory, so each element is read
+// once, in 16-byte pieces (8 bf16), and waits in registers for its row's sum or maximum: a warp
+// to a row of up to 1024 elements, else 256 or 512 threads.  Rows whose pitch, start or length
+// is not a multiple of eight elements go element by element in the same way.
 #include "common.cuh"
 #include "dense.h"
 
 namespace msb {
 namespace {
 
-constexpr int kNT = 256;
-
 __device__ __forceinline__ float load(const void* p, bool f32, int64_t i) {
   return f32 ? static_cast<const float*>(p)[i] : bf16_lo(static_cast<const uint16_t*>(p)[i]);
 }
-
-// Sum over the block, the same value in every thread.
-__device__ float block_sum(float v, float* red) {
-  v = warp_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = 0.f;
-#pragma unroll
-  for (int w = 0; w < kNT / 32; ++w) t += red[w];
-  return t;
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  return (uint32_t)bf16_bits(lo) | (uint32_t)bf16_bits(hi) << 16;
 }
 
-__global__ void __launch_bounds__(kNT) quantize_kernel(const void* x, bool f32, int64_t ldx, int k,
-                                                       int8_t* q, int64_t ldq, float* scale) {
-  __shared__ uint32_t red[kNT / 32];
-  const int64_t row = blockIdx.x;
+// W consecutive elements (8: the address is 16-byte aligned).
+template <int W>
+__device__ __forceinline__ void load_w(const void* p, bool f32, int64_t i, float (&v)[W]) {
+  if constexpr (W == 1) {
+    v[0] = load(p, f32, i);
+  } else if (f32) {
+    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
+    v[4] = bf16_lo(a.z), v[5] = bf16_hi(a.z), v[6] = bf16_lo(a.w), v[7] = bf16_hi(a.w);
+  }
+}
+template <int W>
+__device__ __forceinline__ void store_w(void* p, bool f32, int64_t i, const float (&v)[W]) {
+  if constexpr (W == 1) {
+    if (f32) static_cast<float*>(p)[i] = v[0];
+    else static_cast<uint16_t*>(p)[i] = bf16_bits(v[0]);
+  } else if (f32) {
+    float4* const o = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
+        make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+  }
+}
+
+// Sum (or maximum) over the NT threads of a row, the same value in each.  NT = 32: a warp, else
+// the block; `red` is used once per call site.
+template <int NT>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if constexpr (NT > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) v += red[w];
+  }
+  return v;
+}
+template <int NT>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if constexpr (NT > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) v = max(v, red[w]);
+  }
+  return v;
+}
+
+__host__ __device__ constexpr int block_threads(int nt) { return nt < 256 ? 256 : nt; }
+
+// ------------------------------------------------------------------ 8-bit quantisation
+
+struct QuantScale {
+  float scale, inv;
+};
+__device__ __forceinline__ QuantScale quant_scale(uint32_t big) {
+  const float most = __uint_as_float(big);
+  if (big >= 0x7f800000u) return {__uint_as_float(0x7fc00000u), 0.f};  // an infinity or NaN
+  if (most < 1.504632769e-36f) return {0.f, 0.f};                      // below 2^-119
+  return {most / 127.f, 127.f / most};
+}
+__device__ __forceinline__ int32_t quant(float v, float inv) { return inv == 0.f ? 0 : __float2int_rn(v * inv); }
+
+// V pieces of W elements a thread.
+template <int NT, int W, int V>
+__global__ void __launch_bounds__(block_threads(NT))
+    quantize_kernel(const void* x, bool f32, int64_t ldx, int rows, int k, int8_t* q, int64_t ldq, float* scale) {
+  __shared__ uint32_t red[NT / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t row = (int64_t)blockIdx.x * (block_threads(NT) / NT) + threadIdx.x / NT;
+  if (row >= rows) return;  // whole warps; larger rows have a block each
+  const int tid = threadIdx.x % NT;
+  float v[V][W];
   // largest magnitude as bits: ascending with the value, infinities and NaN on top
   uint32_t big = 0;
-  for (int i = threadIdx.x; i < k; i += kNT)
-    big = max(big, __float_as_uint(load(x, f32, row * ldx + i)) & 0x7fffffffu);
-  big = __reduce_max_sync(0xffffffffu, big);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = big;
-  __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kNT / 32; ++w) big = max(big, red[w]);
-  const float most = __uint_as_float(big);
-  const bool finite = big < 0x7f800000u, zero = most < 1.504632769e-36f;  // 2^-119
-  const float inv = finite && !zero ? 127.f / most : 0.f;
-  if (threadIdx.x == 0) scale[row] = !finite ? __uint_as_float(0x7fc00000u) : zero ? 0.f : most / 127.f;
-  for (int i = threadIdx.x; i < k; i += kNT)
-    q[row * ldq + i] = inv == 0.f ? 0 : (int8_t)__float2int_rn(load(x, f32, row * ldx + i) * inv);
-}
-
-__global__ void __launch_bounds__(kNT)
-    combine_kernel(const void* y, bool f32, int64_t ldy, int y_rows, const int32_t* pos,
-                   const float* weights, int top_e, int d, uint16_t* out, int64_t ldo) {
-  const int64_t t = blockIdx.x;
-  for (int i = threadIdx.x; i < d; i += kNT) {
-    float acc = 0.f;
-    for (int k = 0; k < top_e; ++k) {
-      const int p = pos[t * top_e + k];
-      if (p >= 0 && p < y_rows) acc = fmaf(weights[t * top_e + k], load(y, f32, p * ldy + i), acc);
+  for (int j = 0; j < V; ++j) {
+    const int i = (j * NT + tid) * W;
+    if (i < k) load_w<W>(x, f32, row * ldx + i, v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if ((j * NT + tid) * W < k)
+#pragma unroll
+      for (int c = 0; c < W; ++c) big = max(big, __float_as_uint(v[j][c]) & 0x7fffffffu);
+  const QuantScale qs = quant_scale(row_max<NT>(big, red));
+  if (tid == 0) scale[row] = qs.scale;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int i = (j * NT + tid) * W;
+    if (i >= k) continue;
+    int8_t* const o = q + row * ldq + i;
+    if constexpr (W == 1) {
+      *o = (int8_t)quant(v[j][0], qs.inv);
+    } else {
+      uint32_t lo = 0, hi = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        lo |= (uint32_t)(uint8_t)quant(v[j][c], qs.inv) << (8 * c);
+        hi |= (uint32_t)(uint8_t)quant(v[j][c + 4], qs.inv) << (8 * c);
+      }
+      *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
     }
-    out[t * ldo + i] = __bfloat16_as_ushort(__float2bfloat16_rn(acc));
   }
 }
 
-// b = [rms](y), h' = skip h + residual gate b, x = rms(h'); the row of h' waits in shared
-// memory for its norm.
-__global__ void __launch_bounds__(kNT) block_norm_kernel(const NormArgs a) {
-  extern __shared__ float row[];
-  __shared__ float red[kNT / 32];
-  const int64_t t = blockIdx.x;
-  float yscale = 1.f;
-  if (a.y && a.post_norm) {
-    float ss = 0.f;
-    for (int i = threadIdx.x; i < a.d; i += kNT) {
-      const float v = load(a.y, a.y_f32, t * a.ldy + i);
-      ss = fmaf(v, v, ss);
+// Rows of any length, read twice.
+__global__ void __launch_bounds__(256)
+    quantize_long_kernel(const void* x, bool f32, int64_t ldx, int k, int8_t* q, int64_t ldq, float* scale) {
+  __shared__ uint32_t red[8];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t row = blockIdx.x;
+  uint32_t big = 0;
+  for (int i = threadIdx.x; i < k; i += 256) big = max(big, __float_as_uint(load(x, f32, row * ldx + i)) & 0x7fffffffu);
+  const QuantScale qs = quant_scale(row_max<256>(big, red));
+  if (threadIdx.x == 0) scale[row] = qs.scale;
+  for (int i = threadIdx.x; i < k; i += 256) q[row * ldq + i] = (int8_t)quant(load(x, f32, row * ldx + i), qs.inv);
+}
+
+// ------------------------------------------------------------------ combine
+
+constexpr int kCombineNT = 256;
+
+// A block per (token, run of 256 W columns).
+template <int W>
+__global__ void __launch_bounds__(kCombineNT)
+    combine_kernel(const void* y, bool f32, int64_t ldy, int y_rows, const int32_t* pos, const float* weights,
+                   int top_e, int d, int runs, uint16_t* out, int64_t ldo) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t t = blockIdx.x / runs;
+  const int i = ((int)(blockIdx.x % runs) * kCombineNT + threadIdx.x) * W;
+  if (i >= d) return;
+  float acc[W] = {};
+  for (int k = 0; k < top_e; k += 4) {  // four rows' loads in flight
+    float v[4][W], w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int p = k + j < top_e ? pos[t * top_e + k + j] : -1;
+      w[j] = 0.f;
+      if ((uint32_t)p < (uint32_t)y_rows) {
+        w[j] = weights[t * top_e + k + j];
+        load_w<W>(y, f32, p * ldy + i, v[j]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < W; ++c) v[j][c] = 0.f;
+      }
     }
-    yscale = 1.f / sqrtf(block_sum(ss, red) / (float)a.d + a.eps);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int c = 0; c < W; ++c) acc[c] = fmaf(w[j], v[j][c], acc[c]);
+  }
+  store_w<W>(out, false, t * ldo + i, acc);
+}
+
+// ------------------------------------------------------------------ block norm
+
+// b = [rms](y), h' = skip h + residual gate b, x = rms(h').
+template <int NT, int W, int V>
+__global__ void __launch_bounds__(block_threads(NT)) block_norm_kernel(const NormArgs a) {
+  __shared__ float red[2][NT / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t t = (int64_t)blockIdx.x * (block_threads(NT) / NT) + threadIdx.x / NT;
+  if (t >= a.rows) return;  // whole warps; larger rows have a block each
+  const int tid = threadIdx.x % NT;
+  float h[V][W], y[V][W];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int i = (j * NT + tid) * W;
+    if (i < a.d) {
+      if (a.y) load_w<W>(a.y, a.y_f32, t * a.ldy + i, y[j]);
+      load_w<W>(a.h, a.h_f32, t * a.ldh + i, h[j]);
+    }
+  }
+  float yscale = 1.f;
+  if (a.post_norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if ((j * NT + tid) * W < a.d)
+#pragma unroll
+        for (int c = 0; c < W; ++c) ss = fmaf(y[j][c], y[j][c], ss);
+    yscale = 1.f / sqrtf(row_sum<NT>(ss, red[0]) / (float)a.d + a.eps);
   }
   float ss = 0.f;
-  for (int i = threadIdx.x; i < a.d; i += kNT) {
-    float v = a.skip * load(a.h, a.h_f32, t * a.ldh + i);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int i = (j * NT + tid) * W;
+    if (i >= a.d) continue;
+    float v[W];
+#pragma unroll
+    for (int c = 0; c < W; ++c) v[c] = a.skip * h[j][c];
     if (a.y) {
-      float b = load(a.y, a.y_f32, t * a.ldy + i) * yscale;
-      if (a.post_norm && a.post) b *= load(a.post, a.w_f32, i);
-      if (a.gate) b *= load(a.gate, a.gate_f32, t * a.gate_row + i * a.gate_col);
-      v = fmaf(a.residual, b, v);
+      float b[W], m[W];
+#pragma unroll
+      for (int c = 0; c < W; ++c) b[c] = y[j][c] * yscale;
+      if (a.post) {
+        load_w<W>(a.post, a.w_f32, i, m);
+#pragma unroll
+        for (int c = 0; c < W; ++c) b[c] *= m[c];
+      }
+      if (a.gate) {
+        if (a.gate_col == 0) {
+          const float g = load(a.gate, a.gate_f32, t * a.gate_row);
+#pragma unroll
+          for (int c = 0; c < W; ++c) m[c] = g;
+        } else if (W > 1 && a.gate_col == 1) {
+          load_w<W>(a.gate, a.gate_f32, t * a.gate_row + i, m);
+        } else {
+#pragma unroll
+          for (int c = 0; c < W; ++c) m[c] = load(a.gate, a.gate_f32, t * a.gate_row + (i + c) * a.gate_col);
+        }
+#pragma unroll
+        for (int c = 0; c < W; ++c) b[c] *= m[c];
+      }
+#pragma unroll
+      for (int c = 0; c < W; ++c) v[c] = fmaf(a.residual, b[c], v[c]);
     }
-    row[i] = v;
-    ss = fmaf(v, v, ss);
-    if (a.h_out) {
-      if (a.h_f32) static_cast<float*>(a.h_out)[t * a.ldh_out + i] = v;
-      else static_cast<uint16_t*>(a.h_out)[t * a.ldh_out + i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    }
+#pragma unroll
+    for (int c = 0; c < W; ++c) h[j][c] = v[c], ss = fmaf(v[c], v[c], ss);
+    if (a.h_out) store_w<W>(a.h_out, a.h_f32, t * a.ldh_out + i, v);
   }
   if (!a.x) return;
-  const float inv = 1.f / sqrtf(block_sum(ss, red) / (float)a.d + a.eps);
-  for (int i = threadIdx.x; i < a.d; i += kNT) {
-    float v = row[i] * inv;
-    if (a.pre) v *= load(a.pre, a.w_f32, i);
-    a.x[t * a.ldx + i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  const float inv = 1.f / sqrtf(row_sum<NT>(ss, red[1]) / (float)a.d + a.eps);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int i = (j * NT + tid) * W;
+    if (i >= a.d) continue;
+    float v[W];
+#pragma unroll
+    for (int c = 0; c < W; ++c) v[c] = h[j][c] * inv;
+    if (a.pre) {
+      float m[W];
+      load_w<W>(a.pre, a.w_f32, i, m);
+#pragma unroll
+      for (int c = 0; c < W; ++c) v[c] *= m[c];
+    }
+    store_w<W>(a.x, false, t * a.ldx + i, v);
   }
 }
 
-int done() { return cudaGetLastError() == cudaSuccess ? MSB_OK : MSB_ECUDA; }
+// Rows whose eights of elements are 16-byte aligned (a null pointer is).
+bool by8(const void* p, int64_t pitch, int64_t rows) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows == 1 || pitch % 8 == 0);
+}
+
+// f(NT, W, V) for the smallest shape that holds k elements a row.
+#define MSB_ROW_SHAPES(wide, k, F)                        \
+  if (wide) {                                             \
+    if ((k) <= 256) return F(32, 8, 1);                   \
+    if ((k) <= 512) return F(32, 8, 2);                   \
+    if ((k) <= 1024) return F(32, 8, 4);                  \
+    if ((k) <= 2048) return F(256, 8, 1);                 \
+    if ((k) <= 4096) return F(256, 8, 2);                 \
+    if ((k) <= 8192) return F(256, 8, 4);                 \
+    if ((k) <= 16384) return F(512, 8, 4);                \
+  } else {                                                \
+    if ((k) <= 128) return F(32, 1, 4);                   \
+    if ((k) <= 512) return F(32, 1, 16);                  \
+    if ((k) <= 1024) return F(256, 1, 4);                 \
+    if ((k) <= 4096) return F(256, 1, 16);                \
+    if ((k) <= 16384) return F(512, 1, 32);               \
+  }
 
 }  // namespace
 
 int launch_quantize(const void* x, bool f32, int64_t ldx, int rows, int k, int8_t* q, int64_t ldq,
                     float* scale, cudaStream_t st) {
-  quantize_kernel<<<rows, kNT, 0, st>>>(x, f32, ldx, k, q, ldq, scale);
-  return done();
+  const bool wide = k % 8 == 0 && by8(x, ldx, rows) && reinterpret_cast<uintptr_t>(q) % 8 == 0 &&
+                    (rows == 1 || ldq % 8 == 0);
+#define MSB_QUANT(NT, W, V)                                                                          \
+  launch_early(quantize_kernel<NT, W, V>, ((int64_t)rows * NT + block_threads(NT) - 1) / block_threads(NT), \
+         block_threads(NT), 0, st, x, f32, ldx, rows, k, q, ldq, scale)
+  MSB_ROW_SHAPES(wide, k, MSB_QUANT)
+#undef MSB_QUANT
+  return launch_early(quantize_long_kernel, rows, 256, 0, st, x, f32, ldx, k, q, ldq, scale);
 }
 
 int launch_combine(const void* y, bool f32, int64_t ldy, int y_rows, const int32_t* pos,
                    const float* weights, int tokens, int top_e, int d, uint16_t* out, int64_t ldo,
                    cudaStream_t st) {
-  combine_kernel<<<tokens, kNT, 0, st>>>(y, f32, ldy, y_rows, pos, weights, top_e, d, out, ldo);
-  return done();
+  const bool wide = d % 8 == 0 && by8(y, ldy, y_rows) && by8(out, ldo, tokens);
+  const int runs = (d + kCombineNT * (wide ? 8 : 1) - 1) / (kCombineNT * (wide ? 8 : 1));
+  return launch_early(wide ? combine_kernel<8> : combine_kernel<1>, (int64_t)tokens * runs, kCombineNT, 0, st, y, f32, ldy,
+                y_rows, pos, weights, top_e, d, runs, out, ldo);
 }
 
-int launch_block_norm(const NormArgs& a, int rows, cudaStream_t st) {
-  const size_t smem = 4 * (size_t)a.d;
-  if (smem > 47 * 1024 &&
-      cudaFuncSetAttribute(block_norm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           4 * MSB_NORM_MAX_D) != cudaSuccess)
-    return MSB_ECUDA;
-  block_norm_kernel<<<rows, kNT, smem, st>>>(a);
-  return done();
+int launch_block_norm(const NormArgs& a, cudaStream_t st) {
+  const int64_t rows = a.rows;
+  bool wide = a.d % 8 == 0 && by8(a.h, a.ldh, rows) && by8(a.y, a.y ? a.ldy : 0, rows) &&
+              by8(a.h_out, a.h_out ? a.ldh_out : 0, rows) && by8(a.x, a.x ? a.ldx : 0, rows) &&
+              by8(a.pre, 0, 1) && by8(a.post, 0, 1);
+  if (a.gate && a.gate_col == 1) wide = wide && by8(a.gate, a.gate_row, rows);
+#define MSB_NORM(NT, W, V)                                                                       \
+  launch_early(block_norm_kernel<NT, W, V>, (rows * NT + block_threads(NT) - 1) / block_threads(NT), \
+         block_threads(NT), 0, st, a)
+  MSB_ROW_SHAPES(wide, a.d, MSB_NORM)
+#undef MSB_NORM
+  return MSB_EUNSUPPORTED;  // d <= MSB_NORM_MAX_D
 }
 
 }  // namespace msb

@@ -14,48 +14,75 @@ from . import _lib
 from ._lib import MsbGroupWeights
 from .block import Dims, PackedLayer, _act, _check, _ptr, _stream, _temporaries_on
 
-_TYPES = None
+_raw = None  # torch's current stream of a device as a handle, without a Stream object
+
+
+def _types():
+    import torch
+    global _raw
+    _raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return {torch.bfloat16: _lib.MSB_BF16, torch.float32: _lib.MSB_F32}
+
+
+_TYPES: dict = {}
 
 
 def _type(t, what: str) -> int:
-    global _TYPES
-    if _TYPES is None:
-        import torch
-        _TYPES = {torch.bfloat16: _lib.MSB_BF16, torch.float32: _lib.MSB_F32}
+    if not _TYPES:
+        _TYPES.update(_types())
     code = _TYPES.get(t.dtype)
     if code is None:
         raise ValueError("%s must be bf16 or float32, got %s" % (what, t.dtype))
     return code
 
 
-def _here(lead, *others):
-    """Every tensor on `lead`'s device, which is the current one."""
-    dev = lead.device
-    if dev.type != "cuda":
-        raise ValueError("expected CUDA tensors, got one on %s" % dev)
-    import torch
-    if dev.index != torch.cuda.current_device():
-        raise ValueError("the tensors are on %s but the current device is cuda:%d (the library "
-                         "launches on the current device)" % (dev, torch.cuda.current_device()))
+def _here(lead, *others) -> int:
+    """Every tensor on `lead`'s device, which is the current one; its index."""
+    dev = lead.get_device()
+    if dev < 0:
+        raise ValueError("expected CUDA tensors, got one on %s" % lead.device)
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError("tensors on %s and %s" % (dev, t.device))
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors on %s and %s" % (lead.device, t.device))
+    import torch
+    if dev != torch.cuda.current_device():
+        raise ValueError("the tensors are on cuda:%d but the current device is cuda:%d (the library "
+                         "launches on the current device)" % (dev, torch.cuda.current_device()))
+    return dev
+
+
+def _on(stream, dev: int, new) -> int:
+    """The call's stream as a handle, ordered after the allocation of the buffers `new`."""
+    if stream is None:
+        if _raw is None:
+            _TYPES.update(_types())
+        return _raw(dev)
+    _temporaries_on(stream, new)
+    return _stream(stream)
 
 
 def _rows2d(t, what: str) -> int:
     """Pitch in elements of a 2-d tensor whose last dimension is contiguous."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1 and t.shape[0] > 0):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1 and shape[0] > 0):
         raise ValueError("%s must be 2-d with a contiguous last dimension, got %s strides %s"
-                         % (what, tuple(t.shape), t.stride()))
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+                         % (what, tuple(shape), stride))
+    return stride[0] if shape[0] > 1 else max(shape[1], 1)
 
 
 def _ints(t, numel: int, what: str):
-    if t is not None:
-        import torch
-        if t.dtype != torch.int32 or t.numel() < numel or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous int32 tensor of %d elements, got %s %s"
-                             % (what, numel, t.dtype, tuple(t.shape)))
+    import torch
+    if t.dtype is not torch.int32 or t.numel() < numel or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of %d elements, got %s %s"
+                         % (what, numel, t.dtype, tuple(t.shape)))
+
+
+def _floats(t, shape, what: str):
+    import torch
+    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 tensor %s, got %s %s"
+                         % (what, tuple(shape), t.dtype, tuple(t.shape)))
 
 
 def dense_check(stream=None):
@@ -78,10 +105,27 @@ class Routing:
 
     @classmethod
     def empty(cls, tokens: int, experts: int, top_e: int, device="cuda") -> "Routing":
+        return cls._in(_routing_buffer(tokens, experts, top_e, 0, device), tokens, experts, top_e)
+
+    @classmethod
+    def _in(cls, buf, tokens: int, experts: int, top_e: int) -> "Routing":
         import torch
-        i32 = lambda *shape: torch.empty(shape, dtype=torch.int32, device=device)  # noqa: E731
-        return cls(i32(tokens, top_e), torch.empty((tokens, top_e), dtype=torch.float32, device=device),
-                   i32(experts + 1), i32(tokens * top_e), i32(tokens, top_e))
+        n, shape, stride, part = tokens * top_e, (tokens, top_e), (top_e, 1), buf.as_strided
+        return cls(part(shape, stride, 0), part(shape, stride, n).view(torch.float32),
+                   part((experts + 1,), (1,), 4 * n), part((n,), (1,), 3 * n), part(shape, stride, 2 * n))
+
+
+def _routing_buffer(tokens, experts, top_e, scratch, device):
+    """One allocation for a Routing (and `scratch` bytes behind it)."""
+    import torch
+    return torch.empty(4 * tokens * top_e + experts + 1 + (scratch + 3) // 4, dtype=torch.int32, device=device)
+
+
+def _mask(mask, tokens: int):
+    import torch
+    if (mask.dtype not in (torch.bool, torch.uint8) or tuple(mask.shape) != (tokens,)
+            or not mask.is_contiguous()):
+        raise ValueError("mask must be a contiguous bool or uint8 tensor of %d tokens" % tokens)
 
 
 def route(logits, top_e: int, renorm: bool = True, mask=None, out: Routing | None = None,
@@ -89,80 +133,88 @@ def route(logits, top_e: int, renorm: bool = True, mask=None, out: Routing | Non
     """Top-K experts of each token from its router logits (bf16 or float32 [tokens][experts]),
     their weights, and the pairs sorted by expert.  mask: bool or uint8 [tokens], 0 for tokens
     that take no part.  workspace: uint8 scratch of msb_route_workspace_size bytes."""
-    import torch
     lib = _lib.load()
     ld = _rows2d(logits, "logits")
     T, E = logits.shape
-    new = []
-    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or tuple(mask.shape) != (T,)
-                             or not mask.is_contiguous()):
-        raise ValueError("mask must be a contiguous bool or uint8 tensor of %d tokens" % T)
+    code = _type(logits, "logits")
     if not 1 <= top_e <= E:
         raise ValueError("top_e must lie in 1..%d" % E)
+    n = T * top_e
+    need = lib.msb_route_workspace_size(T, E)
+    if mask is not None:
+        _mask(mask, T)
+    new = []
     if out is None:
-        out = Routing.empty(T, E, top_e, logits.device)
-        new += [out.ids, out.weights, out.offsets, out.rows, out.pos]
+        buf = _routing_buffer(T, E, top_e, need if workspace is None else 0, logits.device)
+        out = Routing._in(buf, T, E, top_e)
+        new.append(buf)
+        base = buf.data_ptr()
+        at = (base, base + 4 * n, base + 16 * n, base + 12 * n, base + 8 * n)
+        ws, nb = base + 4 * (4 * n + E + 1), need
+        dev = _here(logits, mask, workspace)
     else:
-        for name, n in (("ids", T * top_e), ("offsets", E + 1), ("rows", T * top_e), ("pos", T * top_e)):
-            _ints(getattr(out, name), n, "out." + name)
-        if out.weights.dtype != torch.float32 or out.weights.numel() < T * top_e or not out.weights.is_contiguous():
-            raise ValueError("out.weights must be a contiguous float32 tensor of %d elements" % (T * top_e))
-    if workspace is None:
-        workspace = torch.empty(max(1, lib.msb_route_workspace_size(T, E)), dtype=torch.uint8,
-                                device=logits.device)
-        new.append(workspace)
-    _here(logits, mask, out.ids, out.weights, out.offsets, out.rows, out.pos, workspace)
-    _temporaries_on(stream, new)
-    _check(lib.msb_route(logits.data_ptr(), _type(logits, "logits"), ld, _ptr(mask), T, E, top_e,
-                         1 if renorm else 0, out.ids.data_ptr(), out.weights.data_ptr(),
-                         out.offsets.data_ptr(), out.rows.data_ptr(), out.pos.data_ptr(),
-                         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                         _stream(stream)), "msb_route")
+        for name, k in (("ids", n), ("offsets", E + 1), ("rows", n), ("pos", n)):
+            _ints(getattr(out, name), k, "out." + name)
+        _floats(out.weights, (T, top_e), "out.weights")
+        dev = _here(logits, mask, out.ids, out.weights, out.offsets, out.rows, out.pos, workspace)
+        at = tuple(t.data_ptr() for t in (out.ids, out.weights, out.offsets, out.rows, out.pos))
+        if workspace is None:
+            import torch
+            buf = torch.empty(max(1, need), dtype=torch.uint8, device=logits.device)
+            new.append(buf)
+            ws, nb = buf.data_ptr(), need
+    if workspace is not None:
+        ws, nb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = lib.msb_route(logits.data_ptr(), code, ld, _ptr(mask), T, E, top_e, 1 if renorm else 0, *at, ws, nb,
+                       _on(stream, dev, new))
+    if rc:
+        _check(rc, "msb_route")
     return out
 
 
 # ------------------------------------------------------------------ grouped products
 
-def _weights(w, dtype, parts: bool):
+def _weights(w, parts: bool):
     """(msb_group_weights, groups, n, k) of a [groups][n][k] or [groups][2][n][k] tensor (one
     group: without the leading dimension), any strides the C ABI takes."""
-    if w.dtype != dtype:
-        raise ValueError("the weights must be %s, got %s" % (dtype, w.dtype))
+    shape, stride = w.shape, w.stride()
     dims = 3 if parts else 2
-    if w.dim() not in (dims, dims + 1):
+    if len(shape) == dims:
+        shape, stride = (1, *shape), (0, *stride)
+    if len(shape) != dims + 1 or (parts and shape[1] != 2):
         raise ValueError("weights of shape %s: expected %s" % (tuple(w.shape), (
             "[groups][2][n][k]" if parts else "[groups][n][k]")))
-    shape, stride = tuple(w.shape), w.stride()
-    if w.dim() == dims:
-        shape, stride = (1,) + shape, (0,) + stride
-    if parts and shape[1] != 2:
-        raise ValueError("weights of shape %s: the gate and up parts are dimension -3" % (tuple(w.shape),))
-    sn, sk = stride[-2:]
     n, k = shape[-2:]
+    sn, sk = stride[-2:]
     if k == 1 and sn != 1:
         sk = 1
-    return (MsbGroupWeights(w.data_ptr(), stride[0], stride[1] if parts else 0, sn, sk), shape[0], n, k)
+    return MsbGroupWeights(w.data_ptr(), stride[0], stride[1] if parts else 0, sn, sk), shape[0], n, k
 
 
-def _product(fn_name, x, w, offsets, rows, out, out_dtype, stream, parts, scales=None):
+def _product(what, x, w, offsets, rows, out, out_dtype, stream, parts, q_scale=None, w_scale=None, q=None):
+    """One grouped product.  q: quantise x on the way (None: x is what is multiplied)."""
     import torch
-    i8 = scales is not None
-    gw, groups, n, k = _weights(w, torch.int8 if i8 else torch.bfloat16, parts)
-    if x.dtype != w.dtype:
-        raise ValueError("x must be %s, got %s" % (w.dtype, x.dtype))
+    i8 = w_scale is not None
+    gw, groups, n, k = _weights(w, parts)
+    if w.dtype is not (torch.int8 if i8 else torch.bfloat16) or (q is None and x.dtype is not w.dtype):
+        raise ValueError("x is %s and the weights %s" % (x.dtype, w.dtype))
     ldx = _rows2d(x, "x")
-    if x.shape[1] != k:
-        raise ValueError("x has %d columns, the weights %d" % (x.shape[1], k))
-    if offsets is None and groups != 1:
+    R, cols = x.shape
+    if cols != k:
+        raise ValueError("x has %d columns, the weights %d" % (cols, k))
+    if offsets is not None:
+        _ints(offsets, groups + 1, "offsets")
+    elif groups != 1:
         raise ValueError("offsets are required with %d groups" % groups)
-    _ints(offsets, groups + 1, "offsets")
-    r = x.shape[0] if rows is None else rows.numel()
-    _ints(rows, r, "rows")
+    r = R
+    if rows is not None:
+        r = rows.numel()
+        _ints(rows, r, "rows")
     new = []
     if out is None:
-        out = torch.empty((r, n), dtype=out_dtype or torch.bfloat16, device=x.device)
-        new = [out]
-    elif out_dtype is not None and out.dtype != out_dtype:
+        out = torch.empty(r, n, dtype=out_dtype or torch.bfloat16, device=x.device)
+        new.append(out)
+    elif out_dtype is not None and out.dtype is not out_dtype:
         raise ValueError("out is %s, out_dtype %s" % (out.dtype, out_dtype))
     ldo = _rows2d(out, "out")
     # out may have rows behind the last group's; without offsets every row is computed
@@ -171,30 +223,32 @@ def _product(fn_name, x, w, offsets, rows, out, out_dtype, stream, parts, scales
     code = _type(out, "out")
     if parts and code != _lib.MSB_BF16:
         raise ValueError("SwiGLU products are bf16")
-    extra = ()
-    if i8:
-        q_scale, w_scale = scales
-        want = (groups, 2, n) if parts else (groups, n)
-        if q_scale.dtype != torch.float32 or q_scale.numel() != x.shape[0] or not q_scale.is_contiguous():
-            raise ValueError("the rows' scales must be a contiguous float32 tensor of %d" % x.shape[0])
-        if (w_scale.dtype != torch.float32 or not w_scale.is_contiguous() or
-                tuple(w_scale.shape) != (want if w.dim() == len(want) + 1 else want[1:])):
-            raise ValueError("the weights' scales must be contiguous float32 %s" % (want,))
-        _here(x, w, offsets, rows, out, q_scale, w_scale)
-        extra = (q_scale, w_scale)
+    dev = _here(x, w, offsets, rows, out, q_scale, w_scale)
+    off, row, o = _ptr(offsets), _ptr(rows), out.data_ptr()
+    lib = _lib.load()
+    if not i8:
+        fn = lib.msb_grouped_swiglu if parts else lib.msb_grouped_matmul
+        rc = fn(x.data_ptr(), ldx, R, row, off, groups, r, gw, n, k, o, *(() if parts else (code,)), ldo,
+                _on(stream, dev, new))
     else:
-        _here(x, w, offsets, rows, out)
-    _temporaries_on(stream, new)
-    args = [x.data_ptr(), ldx]
-    if i8:
-        args.append(extra[0].data_ptr())
-    args += [x.shape[0], _ptr(rows), _ptr(offsets), groups, r, ctypes.byref(gw)]
-    if i8:
-        args.append(extra[1].data_ptr())
-    args += [n, k, out.data_ptr()]
-    if not parts:
-        args.append(code)
-    _check(getattr(_lib.load(), fn_name)(*args, ldo, _stream(stream)), fn_name)
+        want = (groups, 2, n) if parts else (groups, n)
+        _floats(w_scale, want if w.dim() == len(want) + 1 else want[1:], "the weights' scales")
+        if q is None:
+            _floats(q_scale, (R,), "the rows' scales")
+            fn = lib.msb_int8_swiglu if parts else lib.msb_int8_matmul
+            rc = fn(x.data_ptr(), ldx, q_scale.data_ptr(), R, row, off, groups, r, gw, w_scale.data_ptr(), n, k, o,
+                    *(() if parts else (code,)), ldo, _on(stream, dev, new))
+        else:
+            nb = lib.msb_int8_linear_workspace_size(R, k)
+            if nb == 0:
+                raise ValueError("x of %d rows of %d is beyond the library's limits" % (R, k))
+            ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
+            new.append(ws)
+            rc = lib.msb_int8_linear(x.data_ptr(), _type(x, "x"), ldx, R, row, off, groups, r, gw,
+                                     w_scale.data_ptr(), n, k, 1 if parts else 0, o, code, ldo, ws.data_ptr(), nb,
+                                     _on(stream, dev, new))
+    if rc:
+        _check(rc, what)
     return out
 
 
@@ -203,12 +257,12 @@ def grouped_matmul(x, w, offsets=None, rows=None, out=None, out_dtype=None, stre
     x: bf16 [rows][k]; w: bf16 [groups][n][k] view with n or k contiguous (or [n][k]: one
     group); offsets: int32 [groups + 1]; rows: int32, the row of x of each output row (default:
     itself); out: bf16 or float32 [rows][n], rows of no group are left as they are."""
-    return _product("msb_grouped_matmul", x, w, offsets, rows, out, out_dtype, stream, False)
+    return _product("grouped_matmul", x, w, offsets, rows, out, out_dtype, stream, False)
 
 
 def grouped_swiglu(x, w, offsets=None, rows=None, out=None, stream=None):
     """silu(x @ w[e][0].T) * (x @ w[e][1].T) by groups, bf16; w: bf16 [groups][2][n][k]."""
-    return _product("msb_grouped_swiglu", x, w, offsets, rows, out, None, stream, True)
+    return _product("grouped_swiglu", x, w, offsets, rows, out, None, stream, True)
 
 
 # ------------------------------------------------------------------ 8-bit integers
@@ -221,21 +275,24 @@ def quantize_int8(x, out=None, scale=None, stream=None):
     R, k = x.shape
     new = []
     if out is None:
-        buf = torch.empty((R, (k + 15) // 16 * 16), dtype=torch.int8, device=x.device)
-        out = buf if buf.shape[1] == k else buf[:, :k]
-        new.append(buf)
+        pitch = (k + 15) // 16 * 16
+        out = torch.empty(R, pitch, dtype=torch.int8, device=x.device)
+        new.append(out)
+        if pitch != k:
+            out = out[:, :k]
     if scale is None:
         scale = torch.empty(R, dtype=torch.float32, device=x.device)
         new.append(scale)
-    if out.dtype != torch.int8 or tuple(out.shape) != (R, k):
+    if out.dtype is not torch.int8 or out.shape != x.shape:
         raise ValueError("out must be int8 [%d][%d]" % (R, k))
-    if scale.dtype != torch.float32 or scale.numel() != R or not scale.is_contiguous():
-        raise ValueError("scale must be a contiguous float32 tensor of %d" % R)
+    _floats(scale, (R,), "scale")
     ldq = _rows2d(out, "out")
-    _here(x, out, scale)
-    _temporaries_on(stream, new)
-    _check(_lib.load().msb_int8_quantize(x.data_ptr(), _type(x, "x"), ldx, R, k, out.data_ptr(), ldq,
-                                         scale.data_ptr(), _stream(stream)), "msb_int8_quantize")
+    code = _type(x, "x")
+    dev = _here(x, out, scale)
+    rc = _lib.load().msb_int8_quantize(x.data_ptr(), code, ldx, R, k, out.data_ptr(), ldq, scale.data_ptr(),
+                                       _on(stream, dev, new))
+    if rc:
+        _check(rc, "quantize_int8")
     return out, scale
 
 
@@ -244,20 +301,18 @@ def matmul_int8(q, q_scale, w, w_scale, offsets=None, rows=None, out=None, out_d
     """grouped_matmul (or grouped_swiglu) on 8-bit integers: q int8 [rows][k] with q_scale
     float32 [rows], w int8 like the bf16 weights (k contiguous) with w_scale float32 of w's
     shape without k."""
-    return _product("msb_int8_swiglu" if swiglu else "msb_int8_matmul", q, w, offsets, rows, out,
-                    None if swiglu else out_dtype, stream, swiglu, (q_scale, w_scale))
+    return _product("matmul_int8", q, w, offsets, rows, out, None if swiglu else out_dtype, stream, swiglu,
+                    q_scale, w_scale)
 
 
 def linear_int8(x, w, w_scale, offsets=None, rows=None, out=None, out_dtype=None, stream=None):
     """x (bf16 or float32) quantised row by row and multiplied in 8-bit integers."""
-    q, s = quantize_int8(x, stream=stream)
-    return matmul_int8(q, s, w, w_scale, offsets, rows, out, out_dtype, False, stream)
+    return _product("linear_int8", x, w, offsets, rows, out, out_dtype, stream, False, None, w_scale, True)
 
 
 def swiglu_int8(x, w, w_scale, offsets=None, rows=None, out=None, stream=None):
     """linear_int8 for gate and up ([groups][2][n][k]) with SwiGLU."""
-    q, s = quantize_int8(x, stream=stream)
-    return matmul_int8(q, s, w, w_scale, offsets, rows, out, None, True, stream)
+    return _product("swiglu_int8", x, w, offsets, rows, out, None, stream, True, None, w_scale, True)
 
 
 # ------------------------------------------------------------------ combine, norms
@@ -266,25 +321,33 @@ def combine(y, routing: Routing, out=None, stream=None):
     """out[t] = sum_k weights[t][k] * y[pos[t][k]] (bf16 [tokens][d]); y bf16 or float32."""
     import torch
     ldy = _rows2d(y, "y")
-    if routing.pos.dim() != 2 or routing.weights.shape != routing.pos.shape:
-        raise ValueError("routing.pos and routing.weights must be [tokens][top_e]")
-    T, K = routing.pos.shape
-    _ints(routing.pos, T * K, "routing.pos")
-    if routing.weights.dtype != torch.float32 or not routing.weights.is_contiguous():
-        raise ValueError("routing.weights must be contiguous float32")
+    pos, weights = routing.pos, routing.weights
+    if pos.dim() != 2:
+        raise ValueError("routing.pos must be [tokens][top_e]")
+    T, K = pos.shape
+    _ints(pos, T * K, "routing.pos")
+    _floats(weights, (T, K), "routing.weights")
+    d = y.shape[1]
     new = []
     if out is None:
-        out = torch.empty((T, y.shape[1]), dtype=torch.bfloat16, device=y.device)
-        new = [out]
-    if out.dtype != torch.bfloat16 or tuple(out.shape) != (T, y.shape[1]):
-        raise ValueError("out must be bf16 [%d][%d]" % (T, y.shape[1]))
+        out = torch.empty(T, d, dtype=torch.bfloat16, device=y.device)
+        new.append(out)
+    elif out.dtype is not torch.bfloat16 or out.shape != (T, d):
+        raise ValueError("out must be bf16 [%d][%d]" % (T, d))
     ldo = _rows2d(out, "out")
-    _here(y, routing.pos, routing.weights, out)
-    _temporaries_on(stream, new)
-    _check(_lib.load().msb_combine(y.data_ptr(), _type(y, "y"), ldy, y.shape[0], routing.pos.data_ptr(),
-                                   routing.weights.data_ptr(), T, K, y.shape[1], out.data_ptr(), ldo,
-                                   _stream(stream)), "msb_combine")
+    code = _type(y, "y")
+    dev = _here(y, pos, weights, out)
+    rc = _lib.load().msb_combine(y.data_ptr(), code, ldy, y.shape[0], pos.data_ptr(), weights.data_ptr(), T, K, d,
+                                 out.data_ptr(), ldo, _on(stream, dev, new))
+    if rc:
+        _check(rc, "combine")
     return out
+
+
+def _norm_weight(t, d: int, what: str):
+    if t.shape != (d,) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous tensor of %d elements" % (what, d))
+    return _type(t, what)
 
 
 def block_norm(h, y=None, x=None, h_out=None, pre_weight=None, post_norm: bool = False,
@@ -295,45 +358,52 @@ def block_norm(h, y=None, x=None, h_out=None, pre_weight=None, post_norm: bool =
     float32 [rows][d]; gate: [d], or 2-d and broadcastable to [rows][d]; x: bf16 output
     (allocated when None); h_out: where h' goes (default: h itself).  Returns (h', x)."""
     import torch
-    ldh = _rows2d(h, "h")
-    R, d = h.shape
+    ldh = ldo = _rows2d(h, "h")
+    shape = h.shape
+    R, d = shape
+    hcode = _type(h, "h")
     new = []
     if x is None:
-        x = torch.empty((R, d), dtype=torch.bfloat16, device=h.device)
-        new = [x]
+        x = torch.empty(R, d, dtype=torch.bfloat16, device=h.device)
+        new.append(x)
+    elif x.dtype is not torch.bfloat16 or x.shape != shape:
+        raise ValueError("x must be a bf16 tensor shaped like h")
     if h_out is None:
         h_out = h
-    for name, t in (("y", y), ("x", x), ("h_out", h_out)):
-        if t is not None and t.shape != h.shape:
-            raise ValueError("%s must be shaped like h" % name)
-    if x.dtype != torch.bfloat16 or h_out.dtype != h.dtype:
-        raise ValueError("x must be bf16 and h_out of h's type")
-    wtype = 0
-    for name, t in (("pre_weight", pre_weight), ("post_weight", post_weight)):
-        if t is not None:
-            if tuple(t.shape) != (d,) or not t.is_contiguous():
-                raise ValueError("%s must be a contiguous tensor of %d elements" % (name, d))
-            wtype = _type(t, name)
-    if pre_weight is not None and post_weight is not None and pre_weight.dtype != post_weight.dtype:
-        raise ValueError("pre_weight and post_weight must have one type")
-    gtype = grow = gcol = 0
+    elif h_out is not h:
+        if h_out.dtype is not h.dtype or h_out.shape != shape:
+            raise ValueError("h_out must be shaped like h and of its type")
+        ldo = _rows2d(h_out, "h_out")
+    yp = ycode = ldy = 0
+    if y is not None:
+        if y.shape != shape:
+            raise ValueError("y must be shaped like h")
+        yp, ycode, ldy = y.data_ptr(), _type(y, "y"), _rows2d(y, "y")
+    wcode = prep = postp = 0
+    if pre_weight is not None:
+        wcode, prep = _norm_weight(pre_weight, d, "pre_weight"), pre_weight.data_ptr()
+    if post_weight is not None:
+        code, postp = _norm_weight(post_weight, d, "post_weight"), post_weight.data_ptr()
+        if prep and code != wcode:
+            raise ValueError("pre_weight and post_weight must have one type")
+        wcode = code
+    gp = gcode = grow = gcol = 0
     if gate is not None:
-        gtype = _type(gate, "gate")
-        if gate.dim() == 1 and gate.shape[0] == d:
-            gcol = gate.stride(0)
-        elif gate.dim() == 2 and gate.shape[0] in (1, R) and gate.shape[1] in (1, d):
-            grow = gate.stride(0) if gate.shape[0] > 1 else 0
-            gcol = gate.stride(1) if gate.shape[1] > 1 else 0
+        gp, gcode, gs, gt = gate.data_ptr(), _type(gate, "gate"), gate.shape, gate.stride()
+        if len(gs) == 1 and gs[0] == d:
+            gcol = gt[0]
+        elif len(gs) == 2 and gs[0] in (1, R) and gs[1] in (1, d):
+            grow = gt[0] if gs[0] > 1 else 0
+            gcol = gt[1] if gs[1] > 1 else 0
         else:
-            raise ValueError("gate must be [d] or broadcastable [rows][d], got %s" % (tuple(gate.shape),))
-    _here(h, y, x, h_out, pre_weight, post_weight, gate)
-    _temporaries_on(stream, new)
-    _check(_lib.load().msb_block_norm(
-        h.data_ptr(), _type(h, "h"), ldh, _ptr(y), 0 if y is None else _type(y, "y"),
-        0 if y is None else _rows2d(y, "y"), _ptr(pre_weight), _ptr(post_weight), wtype,
-        1 if post_norm else 0, _ptr(gate), gtype, grow, gcol, skip_scale, residual_scale, eps,
-        h_out.data_ptr(), _rows2d(h_out, "h_out"), x.data_ptr(), _rows2d(x, "x"), R, d,
-        _stream(stream)), "msb_block_norm")
+            raise ValueError("gate must be [d] or broadcastable [rows][d], got %s" % (tuple(gs),))
+    dev = _here(h, x, h_out, y, pre_weight, post_weight, gate)
+    rc = _lib.load().msb_block_norm(
+        h.data_ptr(), hcode, ldh, yp, ycode, ldy, prep, postp, wcode, 1 if post_norm else 0, gp, gcode, grow, gcol,
+        skip_scale, residual_scale, eps, h_out.data_ptr(), ldo, x.data_ptr(), _rows2d(x, "x"), R, d,
+        _on(stream, dev, new))
+    if rc:
+        _check(rc, "block_norm")
     return h_out, x
 
 
@@ -406,9 +476,8 @@ def moe_dense_block(x, layer, out=None, mask=None, workspace: DenseWorkspace | N
     if not int8 and layer.q4:
         raise ValueError("4-bit records: use moe_sparse_block")
     T = x.shape[0]
-    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or tuple(mask.shape) != (T,)
-                             or not mask.is_contiguous()):
-        raise ValueError("mask must be a contiguous bool or uint8 tensor of %d tokens" % T)
+    if mask is not None:
+        _mask(mask, T)
     new = []
     if out is None:
         out = torch.empty_like(x)
@@ -418,10 +487,9 @@ def moe_dense_block(x, layer, out=None, mask=None, workspace: DenseWorkspace | N
     if workspace is None:
         workspace = DenseWorkspace(dims, T, int8, x.device)
         new.append(workspace.buf)
-    _here(x, layer.router_t, out, mask, workspace.buf)
-    _temporaries_on(stream, new)
+    dev = _here(x, layer.router_t, out, mask, workspace.buf)
     lib, cd = _lib.load(), dims.c()
-    tail = (out.data_ptr(), ctypes.byref(cd), workspace.ptr, workspace.nbytes, _stream(stream))
+    tail = (out.data_ptr(), ctypes.byref(cd), workspace.ptr, workspace.nbytes, _on(stream, dev, new))
     head = (x.data_ptr(), T, _ptr(mask), layer.router_t.data_ptr())
     if int8:
         rc = lib.moe_dense_block_int8(*head, layer.gate_up.data_ptr(), layer.gate_up_scale.data_ptr(),
