@@ -2,12 +2,15 @@
 // products (pairs sorted by expert and token), in at most two launches and without atomics on
 // global memory, so that the plan is the same in every run.
 //
-// route_kernel: a block takes a run of consecutive tokens, a warp one token at a time: the
+// route_kernel: a block takes a run of consecutive tokens, a warp two tokens at a time: the
 // experts' logits as order-preserving keys in registers, K rounds of a warp-wide maximum (two
-// redux instructions: the key, then the lowest index that has it); the block counts its pairs
-// per expert.  place_kernel: each block adds up the counts before its own (experts before, then
-// blocks before), and places its pairs: a thread per (expert, run of the block's pairs) counts
-// and then writes the pairs of its expert in order.  Up to kOneBlock tokens one block does both.
+// redux instructions: the key, then the lowest index that has it; the two tokens' chains
+// overlap).  Every chunk of kChunk tokens leaves a bit per (expert, token) in shared memory:
+// the bits below a pair's own are its rank among the block's pairs of that expert, and their
+// number the expert's count.  place_kernel adds the counts of the experts and blocks before.
+// Up to kOneBlock tokens one block does both.
+//
+// Bound by latency: the redux chains (about 120 cycles a round) and the two launches.
 #include "common.cuh"
 #include "dense.h"
 
@@ -15,18 +18,9 @@ namespace msb {
 namespace {
 
 constexpr int kNT = 1024;
-constexpr int kOneBlock = 64;   // tokens up to which a single block routes and places
-constexpr int kChunk = 4096;    // pairs placed at a time
+constexpr int kOneBlock = 64;  // tokens up to which a single block routes and places
+constexpr int kChunk = 128;    // tokens whose bits are held at a time
 constexpr int kMaxE = MSB_MAX_EXPERTS;
-
-struct PlaceShared {
-  int32_t ids[kChunk];
-  int32_t part[kNT];
-  int32_t part2[kNT];
-  int32_t base[kMaxE];  // next row of each expert for this block's pairs
-  int32_t warp[32];
-  int32_t total;
-};
 
 // Key of a logit: ascending with the value, -0 = +0; 0 for NaN and -infinity (no candidate);
 // +infinity as the largest finite float.
@@ -39,168 +33,213 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-__device__ void place(const int32_t* ids, int32_t* rows, int32_t* pos, int32_t* offsets,
-                      const int32_t* hist, int tokens, int experts, int top_e, int per,
-                      PlaceShared& s) {
-  const int b = blockIdx.x, nb = gridDim.x, tid = threadIdx.x;
-  const int lane = tid & 31, warp = tid >> 5;
-  const int epad = (experts + 31) & ~31;
-  const int segs = min(16, kNT / epad);  // threads per expert
-  const int seg = tid / epad, e = tid - seg * epad;
-  const bool mine = seg < segs && e < experts;
-  // counts of each expert in the blocks before this one, and in all
-  int before = 0, all = 0;
-  if (mine)
-    for (int i = seg; i < nb; i += segs) {
-      const int c = hist[(int64_t)i * experts + e];
-      all += c;
-      if (i < b) before += c;
-    }
-  s.part[tid] = all;
-  s.part2[tid] = before;
-  __syncthreads();
-  all = before = 0;
-  if (tid < experts)
-    for (int i = 0; i < segs; ++i) all += s.part[i * epad + tid], before += s.part2[i * epad + tid];
-  // rows of the experts before: exclusive scan of `all` over the threads (tid = expert)
+// First row of each expert: exclusive scan of `all` (thread = expert) over the block.
+__device__ __forceinline__ int rows_before(int all, int32_t* warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = all;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31) s.warp[warp] = inc;
+  if (lane == 31) warps[warp] = inc;
   __syncthreads();
-  int lead = 0;
-  for (int w = 0; w < warp; ++w) lead += s.warp[w];
-  const int off = lead + inc - all;
-  if (tid < experts) {
-    s.base[tid] = off + before;
-    if (b == 0) offsets[tid] = off;
-    if (tid == experts - 1) {
-      s.total = off + all;
-      if (b == 0) offsets[experts] = off + all;
-    }
-  }
-  __syncthreads();
-  const int64_t pairs = (int64_t)tokens * top_e;
-  for (int64_t i = s.total + (int64_t)b * kNT + tid; i < pairs; i += (int64_t)nb * kNT) rows[i] = -1;
-  // this block's pairs, a chunk at a time, in order
-  const int64_t p0 = (int64_t)min(b * per, tokens) * top_e;
-  const int64_t p1 = (int64_t)min((b + 1) * per, tokens) * top_e;
-  for (int64_t c0 = p0; c0 < p1; c0 += kChunk) {
-    const int n = (int)min((int64_t)kChunk, p1 - c0);
-    for (int i = tid; i < n; i += kNT) s.ids[i] = ids[c0 + i];
-    __syncthreads();
-    const int run = (n + segs - 1) / segs;
-    const int i0 = min(seg * run, n), i1 = min(i0 + run, n);
-    int count = 0;
-    if (mine)
-      for (int i = i0; i < i1; ++i) count += s.ids[i] == e;
-    s.part[tid] = count;
-    __syncthreads();
-    if (mine) {
-      int at = s.base[e];
-      for (int i = 0; i < seg; ++i) at += s.part[i * epad + e];
-      if (count)
-        for (int i = i0; i < i1; ++i)
-          if (s.ids[i] == e) {
-            rows[at] = (int32_t)((c0 + i) / top_e);
-            pos[c0 + i] = at++;
-          }
-    }
-    __syncthreads();
-    if (tid < experts)
-      for (int i = 0; i < segs; ++i) s.base[tid] += s.part[i * epad + tid];
-    __syncthreads();
-  }
+  int lead = lane < warp ? warps[lane] : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) lead += __shfl_xor_sync(0xffffffffu, lead, o);
+  return lead + inc - all;
 }
 
-// NV: values a lane holds (experts <= 32 NV).
+// NV: values a lane holds (experts <= 32 NV).  One block: the whole plan.  More: pos holds each
+// pair's rank among the block's, and hist the block's counts.
 template <int NV, bool BF16>
 __global__ void __launch_bounds__(kNT, 1)
     route_kernel(const void* logits, int64_t ld, const uint8_t* mask, int tokens, int experts,
                  int top_e, int renorm, int32_t* ids, float* weights, int32_t* offsets,
                  int32_t* rows, int32_t* pos, int32_t* hist, int per) {
-  __shared__ PlaceShared s;
-  __shared__ int32_t count[kMaxE];
+  __shared__ uint32_t bits[kChunk / 32][kMaxE];
+  __shared__ int32_t count[kMaxE];  // pairs of each expert in the chunks before
+  __shared__ int32_t chosen[kChunk * MSB_MAX_TOP_E];
+  __shared__ int32_t warps[32];
+  __shared__ int32_t total;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = tid; i < kChunk / 32 * kMaxE; i += kNT) (&bits[0][0])[i] = 0;
+  for (int e = tid; e < kMaxE; e += kNT) count[e] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int e = tid; e < experts; e += kNT) count[e] = 0;
   __syncthreads();
   const int t1 = min((int)(blockIdx.x + 1) * per, tokens);
-  for (int t = blockIdx.x * per + warp; t < t1; t += kNT / 32) {
-    uint32_t key[NV];
-    const bool use = !mask || mask[t] != 0;
+  for (int c0 = blockIdx.x * per; c0 < t1; c0 += kChunk) {
+    const int n = min(kChunk, t1 - c0);  // tokens of the chunk
+    for (int u = warp * 2; u < n; u += kNT / 16) {
+      uint32_t key[2][NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = i * 32 + lane;
-      float v = -INFINITY;
-      if (use && e < experts) {
-        if constexpr (BF16)
-          v = bf16_lo(static_cast<const uint16_t*>(logits)[(int64_t)t * ld + e]);
-        else
-          v = static_cast<const float*>(logits)[(int64_t)t * ld + e];
-      }
-      key[i] = logit_key(v);
-    }
-    float top = 0.f, sum = 0.f, w = 0.f;
-    int id = -1;
-    for (int k = 0; k < top_e; ++k) {
-      uint32_t best = 0;
-      int at = 0;
+      for (int j = 0; j < 2; ++j) {
+        const int t = c0 + u + j;
+        const bool use = u + j < n && (!mask || mask[t] != 0);
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (key[i] > best) best = key[i], at = i * 32 + lane;
-      const uint32_t most = __reduce_max_sync(0xffffffffu, best);
-      if (most == 0) break;
-      const int e = __reduce_min_sync(0xffffffffu, best == most ? (uint32_t)at : 0xffffffffu);
-      const float v = key_logit(most);
-      if (k == 0) {
-        top = v;
-        if (!renorm) {
-#pragma unroll
-          for (int i = 0; i < NV; ++i)
-            if (key[i]) sum += expf(key_logit(key[i]) - top);
-          sum = warp_sum(sum);
+        for (int i = 0; i < NV; ++i) {
+          const int e = i * 32 + lane;
+          float v = -INFINITY;
+          if (use && e < experts) {
+            if constexpr (BF16)
+              v = bf16_lo(static_cast<const uint16_t*>(logits)[(int64_t)t * ld + e]);
+            else
+              v = static_cast<const float*>(logits)[(int64_t)t * ld + e];
+          }
+          key[j][i] = logit_key(v);
         }
       }
-      if (lane == k) id = e, w = expf(v - top);
+      float top[2] = {0.f, 0.f}, sum[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
+      int id[2] = {-1, -1};
+      for (int k = 0; k < top_e; ++k) {
+        uint32_t best[2], most[2];
+        int at[2], e[2];
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i * 32 + lane == e) key[i] = 0;
+        for (int j = 0; j < 2; ++j) {
+          best[j] = key[j][0];
+          at[j] = lane;
+#pragma unroll
+          for (int i = 1; i < NV; ++i)
+            if (key[j][i] > best[j]) best[j] = key[j][i], at[j] = i * 32 + lane;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) most[j] = __reduce_max_sync(0xffffffffu, best[j]);
+        if ((most[0] | most[1]) == 0) break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          e[j] = __reduce_min_sync(0xffffffffu, best[j] == most[j] ? (uint32_t)at[j] : 0xffffffffu);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (most[j] == 0) continue;
+          const float v = key_logit(most[j]);
+          if (k == 0) {
+            top[j] = v;
+            if (!renorm) {
+#pragma unroll
+              for (int i = 0; i < NV; ++i)
+                if (key[j][i]) sum[j] += expf(key_logit(key[j][i]) - v);
+              sum[j] = warp_sum(sum[j]);
+            }
+          }
+          if (lane == k) id[j] = e[j], w[j] = expf(v - top[j]);
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (i * 32 + lane == e[j]) key[j][i] = 0;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (renorm) sum[j] = warp_sum(w[j]);
+        const int t = u + j;
+        if (t < n && lane < top_e) {
+          const int64_t at = (int64_t)(c0 + t) * top_e + lane;
+          ids[at] = id[j];
+          weights[at] = id[j] < 0 ? 0.f : w[j] / sum[j];
+          chosen[t * top_e + lane] = id[j];
+          if (id[j] >= 0) atomicOr(&bits[t >> 5][id[j]], 1u << (t & 31));
+        }
+      }
     }
-    if (renorm) sum = warp_sum(w);
-    if (lane < top_e) {
-      const int64_t at = (int64_t)t * top_e + lane;
-      ids[at] = id;
-      weights[at] = id < 0 ? 0.f : w / sum;
-      if (id < 0) pos[at] = -1;
-      else atomicAdd(&count[id], 1);
-    }
-  }
-  __syncthreads();
-  for (int e = tid; e < experts; e += kNT) hist[(int64_t)blockIdx.x * experts + e] = count[e];
-  if (gridDim.x == 1) {
     __syncthreads();
-    place(ids, rows, pos, offsets, hist, tokens, experts, top_e, per, s);
+    // rank of each pair among its expert's (and its row, where this block is all there is)
+    if (gridDim.x == 1) {
+      const int all = tid < experts ? __popc(bits[0][tid]) + __popc(bits[1][tid]) : 0;
+      const int off = rows_before(all, warps);
+      if (tid < experts) {
+        offsets[tid] = off;
+        count[tid] = off;
+        if (tid == experts - 1) offsets[experts] = total = off + all;
+      }
+      __syncthreads();
+    }
+    for (int i = tid; i < n * top_e; i += kNT) {
+      const int e = chosen[i], t = i / top_e;
+      int rank = -1;
+      if (e >= 0) {
+        rank = count[e] + __popc(bits[t >> 5][e] & ((1u << (t & 31)) - 1));
+        for (int q = 0; q < (t >> 5); ++q) rank += __popc(bits[q][e]);
+        if (gridDim.x == 1) rows[rank] = t;
+      }
+      pos[(int64_t)c0 * top_e + i] = rank;
+    }
+    if (gridDim.x == 1) {
+      for (int i = total + tid; i < n * top_e; i += kNT) rows[i] = -1;
+      return;  // one chunk
+    }
+    __syncthreads();
+    for (int e = tid; e < experts; e += kNT)
+#pragma unroll
+      for (int q = 0; q < kChunk / 32; ++q) {
+        count[e] += __popc(bits[q][e]);
+        bits[q][e] = 0;
+      }
+    __syncthreads();
   }
+  if (gridDim.x == 1) {  // no tokens
+    for (int e = tid; e <= experts; e += kNT) offsets[e] = 0;
+    return;
+  }
+  for (int e = tid; e < experts; e += kNT) hist[(int64_t)blockIdx.x * experts + e] = count[e];
 }
 
 __global__ void __launch_bounds__(kNT, 1)
     place_kernel(const int32_t* ids, int32_t* rows, int32_t* pos, int32_t* offsets,
                  const int32_t* hist, int tokens, int experts, int top_e, int per) {
-  __shared__ PlaceShared s;
+  __shared__ int32_t part[2][kNT];
+  __shared__ int32_t base[kMaxE];
+  __shared__ int32_t warps[32];
+  __shared__ int32_t total;
+  const int b = blockIdx.x, nb = gridDim.x, tid = threadIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  place(ids, rows, pos, offsets, hist, tokens, experts, top_e, per, s);
+  // counts of each expert in the blocks before this one, and in all: a thread per (expert,
+  // every segs-th block)
+  const int epad = (experts + 31) & ~31;
+  const int segs = kNT / epad;
+  const int seg = tid / epad, e = tid - seg * epad;
+  int before = 0, all = 0;
+  if (seg < segs && e < experts) {
+#pragma unroll 10
+    for (int i = seg; i < nb; i += segs) {
+      const int c = hist[(int64_t)i * experts + e];
+      all += c;
+      before += i < b ? c : 0;
+    }
+  }
+  part[0][tid] = all;
+  part[1][tid] = before;
+  __syncthreads();
+  all = before = 0;
+  if (tid < experts)
+    for (int i = 0; i < segs; ++i) all += part[0][i * epad + tid], before += part[1][i * epad + tid];
+  const int off = rows_before(all, warps);
+  if (tid < experts) {
+    base[tid] = off + before;
+    if (b == 0) offsets[tid] = off;
+    if (tid == experts - 1) {
+      total = off + all;
+      if (b == 0) offsets[experts] = off + all;
+    }
+  }
+  __syncthreads();
+  const int64_t pairs = (int64_t)tokens * top_e;
+  for (int64_t i = total + (int64_t)b * kNT + tid; i < pairs; i += (int64_t)nb * kNT) rows[i] = -1;
+  const int64_t p0 = (int64_t)min(b * per, tokens) * top_e;
+  const int64_t p1 = (int64_t)min((b + 1) * per, tokens) * top_e;
+  for (int64_t i = p0 + tid; i < p1; i += kNT) {
+    const int id = ids[i];
+    if (id < 0) continue;
+    const int at = base[id] + pos[i];
+    pos[i] = at;
+    rows[at] = (int32_t)(i / top_e);
+  }
 }
 
 }  // namespace
 
 int route_blocks(int tokens) {
-  return tokens <= kOneBlock ? 1 : min(148, (tokens + 31) / 32);
+  return tokens <= kOneBlock ? 1 : min(148, (tokens + 63) / 64);
 }
 
 int launch_route(const void* logits, bool bf16, int64_t ld, const uint8_t* mask, int tokens,
