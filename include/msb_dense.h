@@ -89,7 +89,7 @@ typedef struct msb_group_weights {
  *  x        bf16, x_rows rows ldx elements apart; 16-byte aligned, ldx * 2 a positive multiple
  *           of 16.
  *  rows     row of x for each output row (int32 [out_rows]), or NULL: row(p) = p (x_rows >=
- *           out_rows).  A row outside 0..x_rows-1 reads as zeros.
+ *           out_rows).  x_rows is at least 1 where out_rows is.  A row outside 0..x_rows-1 reads as zeros.
  *  offsets  int32 [groups + 1] on the device, ascending, within 0..out_rows; NULL with
  *           groups = 1: all rows.  (An offset that is not is moved to the nearest that is.)
  *  out_rows rows of out; 0 is allowed and does nothing.

@@ -52,7 +52,7 @@ int grouped_check(GroupedArgs& a, const msb_group_weights* w, int32_t out_type) 
   if (!aligned4({a.rows, a.offsets, a.x_scale, a.w_scale}) || !aligned(a.out, size_of(out_type))) return MSB_EINVAL;
   if (a.x_rows > 1 && (a.ldx < 1 || a.ldx * es % 16)) return MSB_EINVAL;
   if (a.out_rows > 1 && a.ldo < a.n) return MSB_EINVAL;
-  if (!a.rows && a.x_rows < a.out_rows) return MSB_EINVAL;
+  if (a.out_rows > 0 && a.x_rows < (a.rows ? 1 : a.out_rows)) return MSB_EINVAL;
   a.w = w->data;
   a.w_k = w->stride_k, a.w_n = w->stride_n, a.w_part = w->stride_part, a.w_group = w->stride_group;
   const int parts = a.swiglu ? 2 : 1;

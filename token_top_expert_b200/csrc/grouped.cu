@@ -26,6 +26,7 @@
 #include <mutex>
 
 #include "dense.h"
+#include "grouped.cuh"
 #include "grouped.h"
 #include "tc.cuh"
 
@@ -35,48 +36,40 @@ __device__ uint32_t g_dense_err;  // sticky error word, read by msb_dense_check
 
 namespace {
 
-constexpr int kGroupsMax = MSB_MAX_EXPERTS;
 constexpr int kTileM = 256;       // weight rows per CTA pair
-constexpr int kTileN = 256;       // most rows of x per tile
 constexpr int kStageBytes = 128;  // bytes of k per stage (one swizzle row)
-constexpr int kStages = 6;
-constexpr int kABytes = 128 * kStageBytes;           // one CTA's weight rows
-constexpr int kBBytes = kTileN / 2 * kStageBytes;    // one CTA's rows of x
-constexpr int kSplit = 2;                    // gathering warps of a stage
-constexpr int kRowWarps = kSplit * kStages;
-constexpr int kLaneRows = kTileN / 2 / kSplit / 4;  // rows of a gathering thread
-constexpr int kThreads = (6 + kRowWarps) * 32;
+constexpr int kABytes = 128 * kStageBytes;  // one CTA's weight rows of a stage
 
 // Bytes between the staged rows of an epilogue warp's 32 bf16 channels: 64 and 16 more, so that
 // eight rows' 16-byte pieces fall into different banks.
 constexpr int kOutPitch = 80;
 
-struct Shared {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[2], acc_empty[2];
-  uint32_t tmem, dead;
-  int32_t first[kGroupsMax + 1];  // first piece of each group
-  int32_t begin[kGroupsMax + 1];  // first row of each group
-  alignas(16) float scale[4][kTileN];  // 8-bit: scales of the tile's rows of x, per epilogue warp
-  alignas(16) uint8_t out[4][32 * kOutPitch];  // 32 rows of an epilogue warp's channels
-};
-static_assert(offsetof(Shared, scale) % 16 == 0 && offsetof(Shared, out) % 16 == 0 && kOutPitch % 16 == 0,
-              "vector accesses");
-constexpr size_t kSmemBytes = (size_t)kStages * (kABytes + kBBytes) + 1024 + sizeof(Shared);
-static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+// BN: most rows of x per tile.  256 for products bound by the matrix unit; 64 where the groups
+// are small and the weights' bytes are all: the stages shrink, and more of them keep more
+// weight bytes in flight (one SM's 96 KB against 160 KB).
+template <int BN>
+struct Cfg {
+  static constexpr int kStages = BN == 256 ? 6 : 10;
+  static constexpr int kBBytes = BN / 2 * kStageBytes;  // one CTA's rows of x of a stage
+  static constexpr int kStage = kABytes + kBBytes;
+  static constexpr int kSplit = BN == 256 ? 2 : 1;  // gathering warps of a stage
+  static constexpr int kThreads = (6 + kSplit * kStages) * 32;
+  static constexpr int kLaneRows = BN / 2 / kSplit / 4;  // rows of a gathering thread
+  static constexpr int kBoxes = BN == 256 ? 4 : 2;       // x in order: boxes of 16 << i rows
 
-struct KArgs {
-  const uint8_t* x;
-  int64_t pitch;  // bytes between rows of x
-  int32_t x_rows;
-  const int32_t* rows;
-  const int32_t* offsets;
-  int32_t groups, out_rows, n, kbytes, mtiles;
-  const float* x_scale;
-  const float* w_scale;
-  void* out;
-  int64_t ldo;
-  int wide;  // out may be written in 16-byte pieces
+  struct Shared {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint32_t tmem, dead;
+    int32_t first[kGroupsMax + 1];  // first piece of each group
+    int32_t begin[kGroupsMax + 1];  // first row of each group
+    alignas(16) float scale[4][BN];  // 8-bit: scales of the tile's rows of x, per epilogue warp
+    alignas(16) uint8_t out[4][32 * kOutPitch];  // 32 rows of an epilogue warp's channels
+  };
+  static_assert(offsetof(Shared, scale) % 16 == 0 && offsetof(Shared, out) % 16 == 0 && kOutPitch % 16 == 0,
+                "vector accesses");
+  static constexpr size_t kSmemBytes = (size_t)kStages * kStage + 1024 + sizeof(Shared);
+  static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 };
 
 // Tensor maps of x in order: boxes of 16 << i rows.
@@ -105,33 +98,18 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32
 }
 
 struct Tile {
-  int group, m, row0, rows;  // rows of x: [row0, row0 + rows), rows <= 256
+  int group, m, row0, rows;  // rows of x: [row0, row0 + rows), rows <= BN
 };
 
-// Rows and pieces before each group, by one warp: every lane takes a run of groups, a scan
-// over the lanes joins them.  Offsets outside [0, out_rows] or below an earlier one are
-// raised or cut to it, so that no offsets lead outside the buffers.
-__device__ void plan_groups(const KArgs& a, Shared& s, int lane) {
+// Rows and pieces before each group, by one warp: every lane takes a run of groups, scans over
+// the lanes join them.
+template <int BN>
+__device__ void plan_groups(const KArgs& a, typename Cfg<BN>::Shared& s, int lane) {
+  group_begins(a, s.begin, lane);
   const int per = (a.groups + 32) >> 5;  // of groups + 1 offsets
   const int e0 = lane * per, e1 = min(e0 + per, a.groups + 1);
-  int top = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int o = a.offsets ? a.offsets[e] : e ? a.out_rows : 0;
-    top = max(top, min(o, a.out_rows));
-    s.begin[e] = top;
-  }
-  int above = top;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, above, o);
-    if (lane >= o) above = max(above, v);
-  }
-  above = __shfl_up_sync(0xffffffffu, above, 1);
-  if (lane == 0) above = 0;
-  for (int e = e0; e < e1; ++e) s.begin[e] = max(s.begin[e], above);
-  __syncwarp();
   auto pieces = [&](int e) {
-    return e < a.groups ? (s.begin[e + 1] - s.begin[e] + kTileN - 1) / kTileN : 0;
+    return e < a.groups ? (s.begin[e + 1] - s.begin[e] + BN - 1) / BN : 0;
   };
   int sum = 0;
   for (int e = e0; e < e1; ++e) sum += pieces(e);
@@ -150,6 +128,7 @@ __device__ void plan_groups(const KArgs& a, Shared& s, int lane) {
 
 // The tile of index t (t < first[groups] * mtiles).  Inside a group eight weight tiles go
 // over all its pieces before the next eight, so that the pairs at work share both operands.
+template <class Shared>
 __device__ __forceinline__ Tile tile_at(const KArgs& a, const Shared& s, int t) {
   int lo = 0, hi = a.groups;  // first[lo] * mtiles <= t < first[hi] * mtiles
   while (hi - lo > 1) {
@@ -172,14 +151,8 @@ __device__ __forceinline__ Tile tile_at(const KArgs& a, const Shared& s, int t) 
   return tile;
 }
 
-// The accumulator's value as a float; 8-bit: the integer sum times the two scales.
-template <bool I8>
-__device__ __forceinline__ float value(uint32_t v, float row_scale, float scale) {
-  if constexpr (I8) return (float)(int32_t)v * row_scale * scale;
-  return __uint_as_float(v);
-}
-
 // This warp has read all it wants of an accumulator.
+template <class Shared>
 __device__ __forceinline__ void release_acc(Shared& s, int buf, int lane) {
   tc_fence_before();
   __syncwarp();
@@ -187,8 +160,8 @@ __device__ __forceinline__ void release_acc(Shared& s, int buf, int lane) {
 }
 
 // One epilogue warp's 32 channels of the accumulator to float: a lane is a channel.
-template <bool I8>
-__device__ __forceinline__ bool store_f32(const KArgs& a, Shared& s, const Tile& tile, uint32_t tmem, int buf,
+template <int BN, bool I8>
+__device__ __forceinline__ bool store_f32(const KArgs& a, typename Cfg<BN>::Shared& s, const Tile& tile, uint32_t tmem, int buf,
                                           uint32_t phase, uint32_t rank, int warp, int lane) {
   const int ch = tile.m * kTileM + (int)rank * 128 + warp * 32 + lane;
   const float ws = I8 && ch < a.n ? a.w_scale[(int64_t)tile.group * a.n + ch] : 1.f;
@@ -196,7 +169,7 @@ __device__ __forceinline__ bool store_f32(const KArgs& a, Shared& s, const Tile&
   tc_fence_after();
   for (int c0 = 0; c0 < tile.rows; c0 += 32) {
     uint32_t v[32];
-    tmem_ld32(tmem + buf * kTileN + ((uint32_t)(warp * 32) << 16) + c0, v);
+    tmem_ld32(tmem + buf * BN + ((uint32_t)(warp * 32) << 16) + c0, v);
     tmem_ld_wait();
     if (c0 + 32 >= tile.rows) release_acc(s, buf, lane);
     if (ch < a.n) {
@@ -213,8 +186,8 @@ __device__ __forceinline__ bool store_f32(const KArgs& a, Shared& s, const Tile&
 // along the lanes of tensor memory and contiguously in the output, so 32 columns (rows of out)
 // at a time are turned through shared memory (transposing 8x8 stores) and leave as 16-byte
 // pieces; element by element where out is not aligned for that or the channels end.
-template <bool I8, bool GATED>
-__device__ __forceinline__ bool store_bf16(const KArgs& a, Shared& s, const Tile& tile, uint32_t tmem, int buf,
+template <int BN, bool I8, bool GATED>
+__device__ __forceinline__ bool store_bf16(const KArgs& a, typename Cfg<BN>::Shared& s, const Tile& tile, uint32_t tmem, int buf,
                                            uint32_t phase, uint32_t rank, int warp, int lane) {
   constexpr int kCh = GATED ? 16 : 32;  // channels of this warp
   const int ch0 = GATED ? tile.m * 128 + (int)rank * 64 + warp * 16 : tile.m * kTileM + (int)rank * 128 + warp * 32;
@@ -231,7 +204,7 @@ __device__ __forceinline__ bool store_bf16(const KArgs& a, Shared& s, const Tile
   }
   if (!wait_warp(&s.acc_full[buf], phase, &s.dead)) return false;
   tc_fence_after();
-  const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(warp * 32) << 16);
+  const uint32_t acc = tmem + buf * BN + ((uint32_t)(warp * 32) << 16);
   uint8_t* const stage = s.out[warp];
   const int lim = a.n - ch0;  // channels of this warp that exist (may be <= 0)
   for (int c0 = 0; c0 < tile.rows; c0 += 32) {
@@ -258,7 +231,7 @@ __device__ __forceinline__ bool store_bf16(const KArgs& a, Shared& s, const Tile
         const float hi0 = value<I8>(v[i][4 * j + 2], rs[j].x, ws[2 * i + 1]);
         const float hi1 = value<I8>(v[i][4 * j + 3], rs[j].y, ws[2 * i + 1]);
         if constexpr (GATED) {
-          m[0][j] = pack_bf16(lo0 / (1.f + __expf(-lo0)) * hi0, lo1 / (1.f + __expf(-lo1)) * hi1);
+          m[0][j] = pack_bf16(gated(lo0, hi0), gated(lo1, hi1));
         } else {
           m[0][j] = pack_bf16(lo0, lo1);
           m[1][j] = pack_bf16(hi0, hi1);
@@ -295,14 +268,16 @@ __device__ __forceinline__ bool store_bf16(const KArgs& a, Shared& s, const Tile
 
 // I8: 8-bit integers (else bf16).  MMAJOR: the weight's n runs contiguously (bf16 only).
 // GATED: rows of the weight tile alternate in eights, gate and up.  F32: float output.
-template <bool I8, bool MMAJOR, bool GATED, bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int BN, bool I8, bool MMAJOR, bool GATED, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ RowMaps xmaps,
                    const KArgs a) {
+  using C = Cfg<BN>;
+  constexpr int kStages = C::kStages, kSplit = C::kSplit;
   extern __shared__ uint8_t raw[];
   // stages on 1024-byte boundaries (the swizzle's period); same offset in both CTAs
   uint8_t* const stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-  Shared& s = *reinterpret_cast<Shared*>(stages + (size_t)kStages * (kABytes + kBBytes));
+  auto& s = *reinterpret_cast<typename C::Shared*>(stages + (size_t)kStages * C::kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -311,12 +286,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    plan_groups(a, s, lane);
+    plan_groups<BN>(a, s, lane);
   } else if (warp == 4) {
-    tmem_alloc_pair(&s.tmem, 512);
+    tmem_alloc_pair(&s.tmem, 2 * BN);
   } else if (warp == 5 && lane == 0) {
     prefetch_map(&wmap);
-    for (int i = 0; i < 4 && !a.rows; ++i) prefetch_map(&xmaps.map[i]);
+    for (int i = 0; i < C::kBoxes && !a.rows; ++i) prefetch_map(&xmaps.map[i]);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.full[i], a.rows ? 1 + 2 * kSplit : 1);
       mbar_init(&s.empty[i], 1);
@@ -348,7 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
         const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
         if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
-        const uint32_t dst = smem_addr(stages) + st * (kABytes + kBBytes);
+        const uint32_t dst = smem_addr(stages) + st * C::kStage;
         const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
         if constexpr (GATED) {
           // eight channels' gate rows, then their up rows: 16 rows of the tile
@@ -378,12 +353,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = 0; i < nk; ++i) {
         if (!(ok = wait_one(&s.full[st], phase, &s.dead))) break;
         tc_fence_after();
-        const uint32_t pa = smem_addr(stages) + st * (kABytes + kBBytes), pb = pa + kABytes;
+        const uint32_t pa = smem_addr(stages) + st * C::kStage, pb = pa + kABytes;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint64_t da = MMAJOR ? smem_desc(pa + q * 2048, kABytes / 2, 1024)
                                      : smem_desc(pa + q * 32, 16, 1024);
-          mma_pair<I8>(tmem + buf * kTileN, da, smem_desc(pb + q * 32, 16, 1024), idesc,
+          mma_pair<I8>(tmem + buf * BN, da, smem_desc(pb + q * 32, 16, 1024), idesc,
                        i > 0 || q > 0);
         }
         mma_commit_pair(&s.empty[st]);
@@ -398,21 +373,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int st = (warp - 6) / kSplit, part = (warp - 6) % kSplit;
     const int chunk = lane & 7, r0 = lane >> 3;  // 16-byte piece of 128, row of each four
     const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
-    const uint32_t base = smem_addr(stages) + st * (kABytes + kBBytes) + kABytes + r0 * kStageBytes;
+    const uint32_t base = smem_addr(stages) + st * C::kStage + kABytes + r0 * kStageBytes;
     uint32_t phase = 0;
     int at = 0;  // stages before this tile, modulo the ring
     for (int t = pair; ok && t < tiles; t += pairs) {
       const Tile tile = tile_at(a, s, t);
       const int half = ((tile.rows + 31) & ~31) >> 1;  // this CTA's rows of the tile
-      const int mine = half / kSplit;  // this warp's: 8, 16, .. kLaneRows * 4 from part * mine on
+      const int mine = half / kSplit;  // this warp's: 8, 16, .. C::kLaneRows * 4 from part * mine on
       int i = st - at;
       if (i < 0) i += kStages;
       at = (at + nk) % kStages;
       if (i >= nk) continue;
-      const uint8_t* src[kLaneRows];
+      const uint8_t* src[C::kLaneRows];
       uint32_t there = 0;  // rows that exist
 #pragma unroll
-      for (int q = 0; q < kLaneRows; ++q) {
+      for (int q = 0; q < C::kLaneRows; ++q) {
         const int p = (int)rank * half + part * mine + q * 4 + r0;
         const int row = q * 4 < mine && p < tile.rows ? a.rows[tile.row0 + p] : -1;
         const bool use = (uint32_t)row < (uint32_t)a.x_rows;
@@ -426,7 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t valid = left < 0 ? 0 : left > 16 ? 16 : left;
         const int64_t k0 = valid ? (int64_t)i * kStageBytes : 0;
 #pragma unroll
-        for (int q = 0; q < kLaneRows; ++q)
+        for (int q = 0; q < C::kLaneRows; ++q)
           if (q * 4 < mine)
             cp_async16(base + (part * mine + q * 4) * kStageBytes + ((chunk ^ ((q * 4 + r0) & 7)) << 4),
                        src[q] + (there >> q & 1 ? k0 : 0), there >> q & 1 ? valid : 0);
@@ -447,12 +422,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = 0; i < nk; ++i) {
         if (!(ok = wait_one(&s.empty[st], phase ^ 1, &s.dead))) break;
         const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
-        const uint32_t dst = smem_addr(stages) + st * (kABytes + kBBytes) + kABytes;
+        const uint32_t dst = smem_addr(stages) + st * C::kStage + kABytes;
         const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
         // rows behind the group's last belong to the next group: their columns of the
         // accumulator are not stored
 #pragma unroll
-        for (int b = 3; b >= 0; --b)
+        for (int b = C::kBoxes - 1; b >= 0; --b)
           if (half & (16 << b)) {
             const int done = half & ~((32 << b) - 1);
             tma_load_2d(dst + done * kStageBytes, &xmaps.map[b], k0, row0 + done, bar);
@@ -476,9 +451,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // the accumulator is handed back once it has been read, before the last stores
       if constexpr (F32)
-        ok = store_f32<I8>(a, s, tile, tmem, buf, acc_phase, rank, warp, lane);
+        ok = store_f32<BN, I8>(a, s, tile, tmem, buf, acc_phase, rank, warp, lane);
       else
-        ok = store_bf16<I8, GATED>(a, s, tile, tmem, buf, acc_phase, rank, warp, lane);
+        ok = store_bf16<BN, I8, GATED>(a, s, tile, tmem, buf, acc_phase, rank, warp, lane);
       if (++buf == 2) buf = 0, acc_phase ^= 1;
     }
   }
@@ -494,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   if (warp == 4) {
     tc_fence_after();
-    tmem_free_pair(tmem, 512);
+    tmem_free_pair(tmem, 2 * BN);
   }
 }
 
@@ -563,9 +538,9 @@ bool row_maps(const GroupedArgs& a, RowMaps* maps) {
   return true;
 }
 
-template <bool I8, bool MMAJOR, bool GATED, bool F32>
+template <int BN, bool I8, bool MMAJOR, bool GATED, bool F32>
 int launch(const CUtensorMap& map, const RowMaps& xmaps, const KArgs& k, cudaStream_t st) {
-  const auto kernel = grouped_kernel<I8, MMAJOR, GATED, F32>;
+  const auto kernel = grouped_kernel<BN, I8, MMAJOR, GATED, F32>;
   struct Device {
     std::once_flag once;
     cudaError_t rc;
@@ -576,51 +551,45 @@ int launch(const CUtensorMap& map, const RowMaps& xmaps, const KArgs& k, cudaStr
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MSB_ECUDA;
   Device& d = devices[dev];
   std::call_once(d.once, [&] {
-    d.rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    d.rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<BN>::kSmemBytes);
     if (d.rc == cudaSuccess) d.rc = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
   });
   if (d.rc != cudaSuccess) return MSB_ECUDA;
-  // at most one pair per tile: pieces <= groups + rows / 256
-  const int64_t most = ((int64_t)k.groups + k.out_rows / kTileN) * k.mtiles;
+  // at most one pair per tile: pieces <= groups + rows / BN
+  const int64_t most = ((int64_t)k.groups + k.out_rows / BN) * k.mtiles;
   const int64_t mine = (int64_t)k.out_rows * k.mtiles;  // and every piece has a row
   const int pairs = (int)std::min<int64_t>(d.sms / 2, std::min(most, mine));
-  return launch_early(kernel, 2 * pairs, kThreads, kSmemBytes, st, map, xmaps, k);
+  return launch_early(kernel, 2 * pairs, Cfg<BN>::kThreads, Cfg<BN>::kSmemBytes, st, map, xmaps, k);
 }
+
+template <int BN>
+int launch_tile(const GroupedArgs& a, const CUtensorMap& map, const RowMaps& xmaps, const KArgs& k, cudaStream_t st) {
+  if (a.i8) {
+    if (a.swiglu) return launch<BN, true, false, true, false>(map, xmaps, k, st);
+    return a.out_f32 ? launch<BN, true, false, false, true>(map, xmaps, k, st)
+                     : launch<BN, true, false, false, false>(map, xmaps, k, st);
+  }
+  if (a.swiglu) return launch<BN, false, false, true, false>(map, xmaps, k, st);
+  if (a.w_k != 1)
+    return a.out_f32 ? launch<BN, false, true, false, true>(map, xmaps, k, st)
+                     : launch<BN, false, true, false, false>(map, xmaps, k, st);
+  return a.out_f32 ? launch<BN, false, false, false, true>(map, xmaps, k, st)
+                   : launch<BN, false, false, false, false>(map, xmaps, k, st);
+}
+
+// Rows per group, on average, up to which the 64-row tile serves a product.
+constexpr int kFewRows = 32;
 
 }  // namespace
 
 int launch_grouped(const GroupedArgs& a, cudaStream_t st) {
+  const KArgs k = kernel_args(a);
+  if (few_rows(a)) return launch_few(a, k, st);
   CUtensorMap map;
   RowMaps xmaps = {};
   if (!weight_map(a, &map) || !row_maps(a, &xmaps)) return MSB_ECUDA;
-  const int es = a.i8 ? 1 : 2;
-  KArgs k;
-  k.x = static_cast<const uint8_t*>(a.x);
-  k.pitch = a.ldx * es;
-  k.x_rows = a.x_rows;
-  k.rows = a.rows;
-  k.offsets = a.offsets;
-  k.groups = a.groups;
-  k.out_rows = a.out_rows;
-  k.n = a.n;
-  k.kbytes = a.k * es;
-  k.mtiles = a.swiglu ? (a.n + 127) / 128 : (a.n + kTileM - 1) / kTileM;
-  k.x_scale = a.x_scale;
-  k.w_scale = a.w_scale;
-  k.out = a.out;
-  k.ldo = a.ldo;
-  k.wide = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && (a.ldo % 8 == 0 || a.out_rows == 1);
-  if (a.i8) {
-    if (a.swiglu) return launch<true, false, true, false>(map, xmaps, k, st);
-    return a.out_f32 ? launch<true, false, false, true>(map, xmaps, k, st)
-                     : launch<true, false, false, false>(map, xmaps, k, st);
-  }
-  if (a.swiglu) return launch<false, false, true, false>(map, xmaps, k, st);
-  if (a.w_k != 1)
-    return a.out_f32 ? launch<false, true, false, true>(map, xmaps, k, st)
-                     : launch<false, true, false, false>(map, xmaps, k, st);
-  return a.out_f32 ? launch<false, false, false, true>(map, xmaps, k, st)
-                   : launch<false, false, false, false>(map, xmaps, k, st);
+  return (int64_t)a.out_rows <= (int64_t)kFewRows * a.groups ? launch_tile<64>(a, map, xmaps, k, st)
+                                                             : launch_tile<256>(a, map, xmaps, k, st);
 }
 
 int dense_check(cudaStream_t st) {

@@ -58,9 +58,13 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   if constexpr (NT > 32) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.f;
+    if constexpr (NT > 256) {
+      v = warp_sum((threadIdx.x & 31) < NT / 32 ? red[threadIdx.x & 31] : 0.f);
+    } else {
+      v = 0.f;
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) v += red[w];
+      for (int w = 0; w < NT / 32; ++w) v += red[w];
+    }
   }
   return v;
 }
@@ -76,7 +80,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
   return v;
 }
 
-__host__ __device__ constexpr int block_threads(int nt) { return nt < 256 ? 256 : nt; }
+__host__ __device__ constexpr int block_threads(int nt) { return nt == 32 ? 256 : nt; }
 
 // ------------------------------------------------------------------ 8-bit quantisation
 
@@ -149,45 +153,6 @@ __global__ void __launch_bounds__(256)
   for (int i = threadIdx.x; i < k; i += 256) q[row * ldq + i] = (int8_t)quant(load(x, f32, row * ldx + i), qs.inv);
 }
 
-// ------------------------------------------------------------------ combine
-
-constexpr int kCombineNT = 256;
-
-// A block per (token, run of 256 W columns).
-template <int W>
-__global__ void __launch_bounds__(kCombineNT)
-    combine_kernel(const void* y, bool f32, int64_t ldy, int y_rows, const int32_t* pos, const float* weights,
-                   int top_e, int d, int runs, uint16_t* out, int64_t ldo) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t t = blockIdx.x / runs;
-  const int i = ((int)(blockIdx.x % runs) * kCombineNT + threadIdx.x) * W;
-  if (i >= d) return;
-  float acc[W] = {};
-  for (int k = 0; k < top_e; k += 4) {  // four rows' loads in flight
-    float v[4][W], w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int p = k + j < top_e ? pos[t * top_e + k + j] : -1;
-      w[j] = 0.f;
-      if ((uint32_t)p < (uint32_t)y_rows) {
-        w[j] = weights[t * top_e + k + j];
-        load_w<W>(y, f32, p * ldy + i, v[j]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < W; ++c) v[j][c] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int c = 0; c < W; ++c) acc[c] = fmaf(w[j], v[j][c], acc[c]);
-  }
-  store_w<W>(out, false, t * ldo + i, acc);
-}
-
-// ------------------------------------------------------------------ block norm
-
 // Eight elements as they lie in memory.
 template <bool F32>
 struct Raw {
@@ -208,6 +173,65 @@ struct Raw {
     }
   }
 };
+
+// ------------------------------------------------------------------ combine
+
+constexpr int kCombineNT = 256;
+
+// A block per (token, run of 256 pieces), eight rows' pieces in flight.
+template <bool F32>
+__global__ void __launch_bounds__(kCombineNT)
+    combine_kernel(const void* y, int64_t ldy, int y_rows, const int32_t* pos, const float* weights, int top_e, int d,
+                   int runs, uint16_t* out, int64_t ldo) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t t = blockIdx.x / runs;
+  const int i = ((int)(blockIdx.x % runs) * kCombineNT + threadIdx.x) * 8;
+  if (i >= d) return;
+  float acc[8] = {};
+  for (int k = 0; k < top_e; k += 8) {
+    Raw<F32> r[8];
+    float w[8];
+    bool use[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int p = k + j < top_e ? pos[t * top_e + k + j] : -1;
+      use[j] = (uint32_t)p < (uint32_t)y_rows;
+      if (use[j]) r[j].load(y, p * ldy + i);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = use[j] ? weights[t * top_e + k + j] : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (use[j]) {
+        float v[8];
+        r[j].get(v);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = fmaf(w[j], v[c], acc[c]);
+      }
+  }
+  store_w<8>(out, false, t * ldo + i, acc);
+}
+
+// The same element by element.
+__global__ void __launch_bounds__(kCombineNT)
+    combine_any_kernel(const void* y, bool f32, int64_t ldy, int y_rows, const int32_t* pos, const float* weights,
+                       int top_e, int d, int runs, uint16_t* out, int64_t ldo) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t t = blockIdx.x / runs;
+  const int i = (int)(blockIdx.x % runs) * kCombineNT + threadIdx.x;
+  if (i >= d) return;
+  float acc = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < top_e; ++k) {
+    const int p = pos[t * top_e + k];
+    if ((uint32_t)p < (uint32_t)y_rows) acc = fmaf(weights[t * top_e + k], load(y, f32, p * ldy + i), acc);
+  }
+  out[t * ldo + i] = bf16_bits(acc);
+}
+
+// ------------------------------------------------------------------ block norm
 
 // The branch's elements of a row: [rms](y) * post * gate.
 template <int W>
@@ -414,7 +438,7 @@ int norm_rows(const NormArgs& a, cudaStream_t st) {
     if ((k) <= 1024) return F(32, 8, 4);                  \
     if ((k) <= 2048) return F(256, 8, 1);                 \
     if ((k) <= 4096) return F(256, 8, 2);                 \
-    if ((k) <= 8192) return F(256, 8, 4);                 \
+    if ((k) <= 8192) return F(512, 8, 2);                 \
     if ((k) <= 16384) return F(512, 8, 4);                \
   } else {                                                \
     if ((k) <= 128) return F(32, 1, 4);                   \
@@ -443,8 +467,13 @@ int launch_combine(const void* y, bool f32, int64_t ldy, int y_rows, const int32
                    cudaStream_t st) {
   const bool wide = d % 8 == 0 && by8(y, ldy, y_rows) && by8(out, ldo, tokens);
   const int runs = (d + kCombineNT * (wide ? 8 : 1) - 1) / (kCombineNT * (wide ? 8 : 1));
-  return launch_early(wide ? combine_kernel<8> : combine_kernel<1>, (int64_t)tokens * runs, kCombineNT, 0, st, y, f32, ldy,
-                y_rows, pos, weights, top_e, d, runs, out, ldo);
+  const int64_t blocks = (int64_t)tokens * runs;
+  if (blocks > 0x7fffffff) return MSB_EUNSUPPORTED;
+  if (!wide)
+    return launch_early(combine_any_kernel, blocks, kCombineNT, 0, st, y, f32, ldy, y_rows, pos, weights, top_e, d,
+                        runs, out, ldo);
+  return launch_early(f32 ? combine_kernel<true> : combine_kernel<false>, blocks, kCombineNT, 0, st, y, ldy, y_rows,
+                      pos, weights, top_e, d, runs, out, ldo);
 }
 
 int launch_block_norm(const NormArgs& a, cudaStream_t st) {
