@@ -82,7 +82,7 @@ struct RowMaps {
 __device__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t* dead) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1; i < kSpinLimit; ++i) {
-    if (try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if (*(volatile uint32_t*)dead) return false;
     if ((i & 15u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) break;
   }
@@ -91,7 +91,7 @@ __device__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t* dead) {
   return false;
 }
 __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, uint32_t* dead) {
-  return try_wait_cluster(bar, parity) || wait_slow(bar, parity, dead);
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, dead);
 }
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t* dead) {
   return __all_sync(0xffffffffu, wait_one(bar, parity, dead));
@@ -322,50 +322,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
       for (int i = 0; i < nk; ++i) {
         if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
         const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
-        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
         const uint32_t dst = smem_addr(stages) + st * C::kStage;
         const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
-        if constexpr (GATED) {
-          // eight channels' gate rows, then their up rows: 16 rows of the tile
-          if (lane < 8)
-            tma_load_4d(dst + lane * 16 * kStageBytes, &wmap, k0, tile.m * 128 + (int)rank * 64 + lane * 8, 0,
-                        tile.group, bar);
-        } else if constexpr (MMAJOR) {
-          if (lane < 2)
-            tma_load_3d(dst + lane * (kABytes / 2), &wmap, tile.m * kTileM + (int)rank * 128 + lane * 64, k0,
-                        tile.group, bar);
-        } else {
-          if (lane == 0)
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
+          if constexpr (GATED) {
+            // eight channels' gate rows, then their up rows: 16 rows of the tile
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              tma_load_4d(dst + q * 16 * kStageBytes, &wmap, k0, tile.m * 128 + (int)rank * 64 + q * 8, 0, tile.group,
+                          bar);
+          } else if constexpr (MMAJOR) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              tma_load_3d(dst + q * (kABytes / 2), &wmap, tile.m * kTileM + (int)rank * 128 + q * 64, k0, tile.group,
+                          bar);
+          } else {
             tma_load_3d(dst, &wmap, k0, tile.m * kTileM + (int)rank * 128, tile.group, bar);
+          }
         }
+        __syncwarp();
         if (++st == kStages) st = 0, phase ^= 1;
       }
     }
-  } else if (warp == 4 && lane == 0 && rank == 0) {
+  } else if (warp == 4 && rank == 0) {
     // ------------------------------------------------ matrix instructions of the pair
     int st = 0, buf = 0;
     uint32_t phase = 0, acc_phase = 0;
     for (int t = pair; ok && t < tiles; t += pairs) {
       const Tile tile = tile_at(a, s, t);
       const uint32_t idesc = instr_desc(I8 ? 2 : 1, MMAJOR, kTileM, (tile.rows + 31) & ~31);
-      if (!(ok = wait_one(&s.acc_empty[buf], acc_phase ^ 1, &s.dead))) break;
+      if (!(ok = wait_warp(&s.acc_empty[buf], acc_phase ^ 1, &s.dead))) break;
       tc_fence_after();
       for (int i = 0; i < nk; ++i) {
-        if (!(ok = wait_one(&s.full[st], phase, &s.dead))) break;
+        if (!(ok = wait_warp(&s.full[st], phase, &s.dead))) break;
         tc_fence_after();
-        const uint32_t pa = smem_addr(stages) + st * C::kStage, pb = pa + kABytes;
+        const uint32_t pa = smem_addr(stages) + st * C::kStage;
+        const uint64_t da = MMAJOR ? smem_desc(pa, kABytes / 2, 1024) : smem_desc(pa, 16, 1024);
+        const uint64_t db = smem_desc(pa + kABytes, 16, 1024);
+        if (elect_one()) {
+          // steps of 32 bytes of k; m-major: of 16 rows
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint64_t da = MMAJOR ? smem_desc(pa + q * 2048, kABytes / 2, 1024)
-                                     : smem_desc(pa + q * 32, 16, 1024);
-          mma_pair<I8>(tmem + buf * BN, da, smem_desc(pb + q * 32, 16, 1024), idesc,
-                       i > 0 || q > 0);
+          for (int q = 0; q < 4; ++q)
+            mma_pair<I8>(tmem + buf * BN, da + q * (MMAJOR ? 2048 >> 4 : 32 >> 4), db + q * (32 >> 4), idesc,
+                         i > 0 || q > 0);
+          mma_commit_pair(&s.empty[st]);
         }
-        mma_commit_pair(&s.empty[st]);
+        __syncwarp();
         if (++st == kStages) st = 0, phase ^= 1;
       }
       if (!ok) break;
-      mma_commit_pair(&s.acc_full[buf]);
+      if (elect_one()) mma_commit_pair(&s.acc_full[buf]);
+      __syncwarp();
       if (++buf == 2) buf = 0, acc_phase ^= 1;
     }
   } else if (warp >= 6 && a.rows) {
@@ -411,7 +419,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
         if (lane == 0) arrive_pair(bar);
       }
     }
-  } else if (warp == 6 && !a.rows && lane == 0) {
+  } else if (warp == 6 && !a.rows) {
     // ------------------------------------------------ rows of x, as they lie
     int st = 0;
     uint32_t phase = 0;
@@ -420,18 +428,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
       const int half = ((tile.rows + 31) & ~31) >> 1;
       const int row0 = tile.row0 + (int)rank * half;
       for (int i = 0; i < nk; ++i) {
-        if (!(ok = wait_one(&s.empty[st], phase ^ 1, &s.dead))) break;
+        if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
         const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
         const uint32_t dst = smem_addr(stages) + st * C::kStage + kABytes;
         const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
         // rows behind the group's last belong to the next group: their columns of the
         // accumulator are not stored
+        if (elect_one()) {
 #pragma unroll
-        for (int b = C::kBoxes - 1; b >= 0; --b)
-          if (half & (16 << b)) {
-            const int done = half & ~((32 << b) - 1);
-            tma_load_2d(dst + done * kStageBytes, &xmaps.map[b], k0, row0 + done, bar);
-          }
+          for (int b = C::kBoxes - 1; b >= 0; --b)
+            if (half & (16 << b)) {
+              const int done = half & ~((32 << b) - 1);
+              tma_load_2d(dst + done * kStageBytes, &xmaps.map[b], k0, row0 + done, bar);
+            }
+        }
+        __syncwarp();
         if (++st == kStages) st = 0, phase ^= 1;
       }
     }
