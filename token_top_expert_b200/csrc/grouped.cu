@@ -49,13 +49,13 @@ constexpr int kOutPitch = 80;
 // weight bytes in flight (one SM's 96 KB against 160 KB).
 template <int BN>
 struct Cfg {
-  static constexpr int kStages = BN == 256 ? 6 : 10;
+  static constexpr int kStages = BN == 256 ? 6 : BN == 128 ? 8 : 10;
   static constexpr int kBBytes = BN / 2 * kStageBytes;  // one CTA's rows of x of a stage
   static constexpr int kStage = kABytes + kBBytes;
   static constexpr int kSplit = BN == 256 ? 2 : 1;  // gathering warps of a stage
   static constexpr int kThreads = (6 + kSplit * kStages) * 32;
   static constexpr int kLaneRows = BN / 2 / kSplit / 4;  // rows of a gathering thread
-  static constexpr int kBoxes = BN == 256 ? 4 : 2;       // x in order: boxes of 16 << i rows
+  static constexpr int kBoxes = BN == 256 ? 4 : BN == 128 ? 3 : 2;       // x in order: boxes of 16 << i rows
 
   struct Shared {
     uint64_t full[kStages], empty[kStages];
@@ -384,24 +384,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
     const uint32_t base = smem_addr(stages) + st * C::kStage + kABytes + r0 * kStageBytes;
     uint32_t phase = 0;
     int at = 0;  // stages before this tile, modulo the ring
-    for (int t = pair; ok && t < tiles; t += pairs) {
+    int next[C::kLaneRows], half = 0, nhalf = 0;  // row indices are fetched a tile ahead
+    const auto fetch = [&](int t) {
+      if (t >= tiles) return;
       const Tile tile = tile_at(a, s, t);
-      const int half = ((tile.rows + 31) & ~31) >> 1;  // this CTA's rows of the tile
+      nhalf = ((tile.rows + 31) & ~31) >> 1;  // this CTA's rows of the tile
+      const int p0 = (int)rank * nhalf + part * (nhalf / kSplit) + r0;
+#pragma unroll
+      for (int q = 0; q < C::kLaneRows; ++q)
+        next[q] = q * 4 < nhalf / kSplit && p0 + q * 4 < tile.rows ? a.rows[tile.row0 + p0 + q * 4] : -1;
+    };
+    fetch(pair);
+    for (int t = pair; ok && t < tiles; t += pairs) {
+      half = nhalf;
       const int mine = half / kSplit;  // this warp's: 8, 16, .. C::kLaneRows * 4 from part * mine on
-      int i = st - at;
-      if (i < 0) i += kStages;
-      at = (at + nk) % kStages;
-      if (i >= nk) continue;
       const uint8_t* src[C::kLaneRows];
       uint32_t there = 0;  // rows that exist
 #pragma unroll
       for (int q = 0; q < C::kLaneRows; ++q) {
-        const int p = (int)rank * half + part * mine + q * 4 + r0;
-        const int row = q * 4 < mine && p < tile.rows ? a.rows[tile.row0 + p] : -1;
-        const bool use = (uint32_t)row < (uint32_t)a.x_rows;
+        const bool use = (uint32_t)next[q] < (uint32_t)a.x_rows;
         there |= (uint32_t)use << q;
-        src[q] = a.x + (use ? (int64_t)row * a.pitch + chunk * 16 : 0);
+        src[q] = a.x + (use ? (int64_t)next[q] * a.pitch + chunk * 16 : 0);
       }
+      fetch(t + pairs);
+      int i = st - at;
+      if (i < 0) i += kStages;
+      at = (at + nk) % kStages;
       for (; i < nk; i += kStages) {
         if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
         phase ^= 1;
@@ -588,8 +596,8 @@ int launch_tile(const GroupedArgs& a, const CUtensorMap& map, const RowMaps& xma
                    : launch<BN, false, false, false, false>(map, xmaps, k, st);
 }
 
-// Rows per group, on average, up to which the 64-row tile serves a product.
-constexpr int kFewRows = 32;
+// Rows per group, on average, up to which the 64- and the 128-row tile serve a product.
+constexpr int kRows64 = 32, kRows128 = 96;
 
 }  // namespace
 
@@ -599,8 +607,10 @@ int launch_grouped(const GroupedArgs& a, cudaStream_t st) {
   CUtensorMap map;
   RowMaps xmaps = {};
   if (!weight_map(a, &map) || !row_maps(a, &xmaps)) return MSB_ECUDA;
-  return (int64_t)a.out_rows <= (int64_t)kFewRows * a.groups ? launch_tile<64>(a, map, xmaps, k, st)
-                                                             : launch_tile<256>(a, map, xmaps, k, st);
+  const int64_t rows = a.out_rows;
+  if (rows <= (int64_t)kRows64 * a.groups) return launch_tile<64>(a, map, xmaps, k, st);
+  if (rows <= (int64_t)kRows128 * a.groups) return launch_tile<128>(a, map, xmaps, k, st);
+  return launch_tile<256>(a, map, xmaps, k, st);
 }
 
 int dense_check(cudaStream_t st) {

@@ -9,12 +9,23 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 
 from . import _lib
 from ._lib import MsbGroupWeights
 from .block import Dims, PackedLayer, _act, _check, _ptr, _stream, _temporaries_on
 
 _raw = None  # torch's current stream of a device as a handle, without a Stream object
+
+
+@functools.lru_cache(maxsize=256)
+def _route_bytes(tokens: int, experts: int) -> int:
+    return _lib.load().msb_route_workspace_size(tokens, experts)
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_bytes(rows: int, k: int) -> int:
+    return _lib.load().msb_int8_linear_workspace_size(rows, k)
 
 
 def _types():
@@ -140,7 +151,7 @@ def route(logits, top_e: int, renorm: bool = True, mask=None, out: Routing | Non
     if not 1 <= top_e <= E:
         raise ValueError("top_e must lie in 1..%d" % E)
     n = T * top_e
-    need = lib.msb_route_workspace_size(T, E)
+    need = _route_bytes(T, E)
     if mask is not None:
         _mask(mask, T)
     new = []
@@ -239,7 +250,7 @@ def _product(what, x, w, offsets, rows, out, out_dtype, stream, parts, q_scale=N
             rc = fn(x.data_ptr(), ldx, q_scale.data_ptr(), R, row, off, groups, r, gw, w_scale.data_ptr(), n, k, o,
                     *(() if parts else (code,)), ldo, _on(stream, dev, new))
         else:
-            nb = lib.msb_int8_linear_workspace_size(R, k)
+            nb = _linear_bytes(R, k)
             if nb == 0:
                 raise ValueError("x of %d rows of %d is beyond the library's limits" % (R, k))
             ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
