@@ -596,8 +596,19 @@ int launch_tile(const GroupedArgs& a, const CUtensorMap& map, const RowMaps& xma
                    : launch<BN, false, false, false, false>(map, xmaps, k, st);
 }
 
-// Rows per group, on average, up to which the 64- and the 128-row tile serve a product.
-constexpr int kRows64 = 32, kRows128 = 96;
+// Rows of the tile that serves a product.
+int tile_rows(const GroupedArgs& a, const KArgs& k) {
+  const int64_t rows = a.out_rows, pairs = 74, groups = std::min<int64_t>(a.groups, rows);
+  // Few tiles: the smallest that one round of the pairs holds (one 4096 x 4096 bf16 weight, 64-,
+  // 128- and 256-row tiles: 256 rows 19.0, 19.8, 26.4 us; 512 rows 31.9, 20.0, 27.4; 1024 rows
+  // 57, 34, 28).
+  for (int bn = 64; bn <= 256; bn *= 2)
+    if (k.mtiles * std::max(groups, (rows + bn - 1) / bn) <= pairs) return bn;
+  // Many: by the rows of a group, on average (gate and up of hidden 2048 x 768 channels x 128
+  // experts; bf16, 32 rows 131, 129, 137 us; 64 rows 176, 148, 147; 128 rows 256, 199, 167; 8
+  // bits, 16 rows 67, 75, 94; 64 rows 91, 88, 128; 128 rows 137, 120, 125).
+  return rows <= 32 * groups ? 64 : rows <= (a.i8 ? 128 : 64) * groups ? 128 : 256;
+}
 
 }  // namespace
 
@@ -607,10 +618,11 @@ int launch_grouped(const GroupedArgs& a, cudaStream_t st) {
   CUtensorMap map;
   RowMaps xmaps = {};
   if (!weight_map(a, &map) || !row_maps(a, &xmaps)) return MSB_ECUDA;
-  const int64_t rows = a.out_rows;
-  if (rows <= (int64_t)kRows64 * a.groups) return launch_tile<64>(a, map, xmaps, k, st);
-  if (rows <= (int64_t)kRows128 * a.groups) return launch_tile<128>(a, map, xmaps, k, st);
-  return launch_tile<256>(a, map, xmaps, k, st);
+  switch (tile_rows(a, k)) {
+    case 64: return launch_tile<64>(a, map, xmaps, k, st);
+    case 128: return launch_tile<128>(a, map, xmaps, k, st);
+    default: return launch_tile<256>(a, map, xmaps, k, st);
+  }
 }
 
 int dense_check(cudaStream_t st) {

@@ -55,8 +55,10 @@ __device__ __forceinline__ float value(uint32_t v, float row_scale, float scale)
   return __uint_as_float(v);
 }
 
-// silu(g) * u.
-__device__ __forceinline__ float gated(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+// silu(g) * u, with the approximate exponential and reciprocal (2^-20 relative; zero below
+// g = -87.3, where silu is under 2e-36): the exact quotient made the epilogue of a 256-row tile
+// 10 us.
+__device__ __forceinline__ float gated(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
 inline KArgs kernel_args(const GroupedArgs& a) {
   const int es = a.i8 ? 1 : 2;
