@@ -67,7 +67,7 @@ int grouped_check(GroupedArgs& a, const msb_group_weights* w, int32_t out_type) 
   if (a.groups == 1) a.w_group = unit;
   for (int64_t s : {*outer, a.w_part, a.w_group})
     if (s <= 0 || s % unit || s * es >= kMaxStride) return MSB_EINVAL;
-  const int64_t tiles = ((int64_t)a.groups + a.out_rows / 256) * (((int64_t)parts * a.n + 255) / 256);
+  const int64_t tiles = ((int64_t)a.groups + a.out_rows / 64) * (((int64_t)parts * a.n + 255) / 256);
   if (tiles >= (int64_t)1 << 30) return MSB_EUNSUPPORTED;
   const int64_t out_bytes = extent(a.out_rows, a.ldo, a.n, size_of(out_type));
   const int64_t w_bytes = ((a.groups - 1) * a.w_group + (parts - 1) * a.w_part +

@@ -40,6 +40,14 @@ constexpr int kTileM = 256;       // weight rows per CTA pair
 constexpr int kStageBytes = 128;  // bytes of k per stage (one swizzle row)
 constexpr int kABytes = 128 * kStageBytes;  // one CTA's weight rows of a stage
 
+// Float outputs of bf16 products: the matrix unit cuts off each addition to its accumulator, by
+// about 1e-9 of the sum per k, always towards zero (measured: 1.5e-6 at k = 1536, 9e-6 at 8192).
+// That is far below bf16's rounding, but not float's, so there the accumulator takes
+// kExactStages stages (256 k, 2e-7) at a time and the epilogue sums them rounded to nearest.
+template <bool I8, bool F32>
+constexpr bool kExact = F32 && !I8;
+constexpr int kExactStages = 4;
+
 // Bytes between the staged rows of an epilogue warp's 32 bf16 channels: 64 and 16 more, so that
 // eight rows' 16-byte pieces fall into different banks.
 constexpr int kOutPitch = 80;
@@ -159,25 +167,53 @@ __device__ __forceinline__ void release_acc(Shared& s, int buf, int lane) {
   if (lane == 0) arrive_pair(map_to(smem_addr(&s.acc_empty[buf]), 0));
 }
 
-// One epilogue warp's 32 channels of the accumulator to float: a lane is a channel.
+// One epilogue warp's 32 channels to float: a lane is a channel.  8-bit sums are exact; bf16
+// products come in parts of kExactStages stages, which are summed here.
 template <int BN, bool I8>
-__device__ __forceinline__ bool store_f32(const KArgs& a, typename Cfg<BN>::Shared& s, const Tile& tile, uint32_t tmem, int buf,
-                                          uint32_t phase, uint32_t rank, int warp, int lane) {
+__device__ __forceinline__ bool store_f32(const KArgs& a, typename Cfg<BN>::Shared& s, const Tile& tile, uint32_t tmem,
+                                          int& buf, uint32_t& phase, int nk, uint32_t rank, int warp, int lane) {
   const int ch = tile.m * kTileM + (int)rank * 128 + warp * 32 + lane;
-  const float ws = I8 && ch < a.n ? a.w_scale[(int64_t)tile.group * a.n + ch] : 1.f;
-  if (!wait_warp(&s.acc_full[buf], phase, &s.dead)) return false;
-  tc_fence_after();
-  for (int c0 = 0; c0 < tile.rows; c0 += 32) {
-    uint32_t v[32];
-    tmem_ld32(tmem + buf * BN + ((uint32_t)(warp * 32) << 16) + c0, v);
-    tmem_ld_wait();
-    if (c0 + 32 >= tile.rows) release_acc(s, buf, lane);
-    if (ch < a.n) {
-      float* const out = static_cast<float*>(a.out) + (int64_t)(tile.row0 + c0) * a.ldo + ch;
+  float* const out = static_cast<float*>(a.out) + (int64_t)tile.row0 * a.ldo + ch;
+  const uint32_t acc = tmem + ((uint32_t)(warp * 32) << 16);
+  if constexpr (I8) {
+    const float ws = ch < a.n ? a.w_scale[(int64_t)tile.group * a.n + ch] : 0.f;
+    if (!wait_warp(&s.acc_full[buf], phase, &s.dead)) return false;
+    tc_fence_after();
+    for (int c0 = 0; c0 < tile.rows; c0 += 32) {
+      uint32_t v[32];
+      tmem_ld32(acc + buf * BN + c0, v);
+      tmem_ld_wait();
+      if (c0 + 32 >= tile.rows) release_acc(s, buf, lane);
+      if (ch < a.n)
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
-        if (c0 + c < tile.rows) out[(int64_t)c * a.ldo] = value<I8>(v[c], s.scale[warp][c0 + c], ws);
+        for (int c = 0; c < 32; ++c)
+          if (c0 + c < tile.rows) out[(int64_t)(c0 + c) * a.ldo] = value<true>(v[c], s.scale[warp][c0 + c], ws);
     }
+    if (++buf == 2) buf = 0, phase ^= 1;
+  } else {
+    static_assert(BN == 64, "the sums of a tile are held in registers");
+    float sum[BN];
+#pragma unroll
+    for (int c = 0; c < BN; ++c) sum[c] = 0.f;
+    for (int i = 0; i < nk; i += kExactStages) {
+      if (!wait_warp(&s.acc_full[buf], phase, &s.dead)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int c0 = 0; c0 < BN; c0 += 32)
+        if (c0 < tile.rows) {
+          uint32_t v[32];
+          tmem_ld32(acc + buf * BN + c0, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) sum[c0 + c] += __uint_as_float(v[c]);
+        }
+      release_acc(s, buf, lane);
+      if (++buf == 2) buf = 0, phase ^= 1;
+    }
+    if (ch < a.n)
+#pragma unroll
+      for (int c = 0; c < BN; ++c)
+        if (c < tile.rows) out[(int64_t)c * a.ldo] = sum[c];
   }
   return true;
 }
@@ -349,32 +385,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
     // ------------------------------------------------ matrix instructions of the pair
     int st = 0, buf = 0;
     uint32_t phase = 0, acc_phase = 0;
+    const int chunk = kExact<I8, F32> ? kExactStages : nk;  // stages summed in one accumulator
     for (int t = pair; ok && t < tiles; t += pairs) {
       const Tile tile = tile_at(a, s, t);
       const uint32_t idesc = instr_desc(I8 ? 2 : 1, MMAJOR, kTileM, (tile.rows + 31) & ~31);
-      if (!(ok = wait_warp(&s.acc_empty[buf], acc_phase ^ 1, &s.dead))) break;
-      tc_fence_after();
-      for (int i = 0; i < nk; ++i) {
-        if (!(ok = wait_warp(&s.full[st], phase, &s.dead))) break;
+      for (int i0 = 0; ok && i0 < nk; i0 += chunk) {
+        if (!(ok = wait_warp(&s.acc_empty[buf], acc_phase ^ 1, &s.dead))) break;
         tc_fence_after();
-        const uint32_t pa = smem_addr(stages) + st * C::kStage;
-        const uint64_t da = MMAJOR ? smem_desc(pa, kABytes / 2, 1024) : smem_desc(pa, 16, 1024);
-        const uint64_t db = smem_desc(pa + kABytes, 16, 1024);
-        if (elect_one()) {
-          // steps of 32 bytes of k; m-major: of 16 rows
+        for (int i = i0; i < min(i0 + chunk, nk); ++i) {
+          if (!(ok = wait_warp(&s.full[st], phase, &s.dead))) break;
+          tc_fence_after();
+          const uint32_t pa = smem_addr(stages) + st * C::kStage;
+          const uint64_t da = MMAJOR ? smem_desc(pa, kABytes / 2, 1024) : smem_desc(pa, 16, 1024);
+          const uint64_t db = smem_desc(pa + kABytes, 16, 1024);
+          if (elect_one()) {
+            // steps of 32 bytes of k; m-major: of 16 rows
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mma_pair<I8>(tmem + buf * BN, da + q * (MMAJOR ? 2048 >> 4 : 32 >> 4), db + q * (32 >> 4), idesc,
-                         i > 0 || q > 0);
-          mma_commit_pair(&s.empty[st]);
+            for (int q = 0; q < 4; ++q)
+              mma_pair<I8>(tmem + buf * BN, da + q * (MMAJOR ? 2048 >> 4 : 32 >> 4), db + q * (32 >> 4), idesc,
+                           i > i0 || q > 0);
+            mma_commit_pair(&s.empty[st]);
+          }
+          __syncwarp();
+          if (++st == kStages) st = 0, phase ^= 1;
         }
+        if (!ok) break;
+        if (elect_one()) mma_commit_pair(&s.acc_full[buf]);
         __syncwarp();
-        if (++st == kStages) st = 0, phase ^= 1;
+        if (++buf == 2) buf = 0, acc_phase ^= 1;
       }
-      if (!ok) break;
-      if (elect_one()) mma_commit_pair(&s.acc_full[buf]);
-      __syncwarp();
-      if (++buf == 2) buf = 0, acc_phase ^= 1;
     }
   } else if (warp >= 6 && a.rows) {
     // ------------------------------------------------ rows of x, gathered
@@ -469,11 +508,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
         __syncwarp();
       }
       // the accumulator is handed back once it has been read, before the last stores
-      if constexpr (F32)
-        ok = store_f32<BN, I8>(a, s, tile, tmem, buf, acc_phase, rank, warp, lane);
-      else
+      if constexpr (F32) {
+        ok = store_f32<BN, I8>(a, s, tile, tmem, buf, acc_phase, nk, rank, warp, lane);
+      } else {
         ok = store_bf16<BN, I8, GATED>(a, s, tile, tmem, buf, acc_phase, rank, warp, lane);
-      if (++buf == 2) buf = 0, acc_phase ^= 1;
+        if (++buf == 2) buf = 0, acc_phase ^= 1;
+      }
     }
   }
   __syncwarp();
@@ -589,15 +629,17 @@ int launch_tile(const GroupedArgs& a, const CUtensorMap& map, const RowMaps& xma
                      : launch<BN, true, false, false, false>(map, xmaps, k, st);
   }
   if (a.swiglu) return launch<BN, false, false, true, false>(map, xmaps, k, st);
-  if (a.w_k != 1)
-    return a.out_f32 ? launch<BN, false, true, false, true>(map, xmaps, k, st)
-                     : launch<BN, false, true, false, false>(map, xmaps, k, st);
-  return a.out_f32 ? launch<BN, false, false, false, true>(map, xmaps, k, st)
-                   : launch<BN, false, false, false, false>(map, xmaps, k, st);
+  if constexpr (BN == 64)
+    if (a.out_f32)
+      return a.w_k != 1 ? launch<BN, false, true, false, true>(map, xmaps, k, st)
+                        : launch<BN, false, false, false, true>(map, xmaps, k, st);
+  return a.w_k != 1 ? launch<BN, false, true, false, false>(map, xmaps, k, st)
+                    : launch<BN, false, false, false, false>(map, xmaps, k, st);
 }
 
 // Rows of the tile that serves a product.
 int tile_rows(const GroupedArgs& a, const KArgs& k) {
+  if (a.out_f32 && !a.i8) return 64;  // sums in registers
   const int64_t rows = a.out_rows, pairs = 74, groups = std::min<int64_t>(a.groups, rows);
   // Few tiles: the smallest that one round of the pairs holds (one 4096 x 4096 bf16 weight, 64-,
   // 128- and 256-row tiles: 256 rows 19.0, 19.8, 26.4 us; 512 rows 31.9, 20.0, 27.4; 1024 rows
