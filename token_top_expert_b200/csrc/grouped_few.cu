@@ -187,11 +187,15 @@ int launch(const GroupedArgs& a, const KArgs& k, cudaStream_t st) {
 
 }  // namespace
 
-// Up to 12 rows, or a row per group on average, this kernel is the faster one (the matrix unit's
-// in brackets, cold weights): gate and up of hidden 2048 x 768 channels x 128 experts top-8, 1
-// token 11.9 us (20.4), 4 tokens 33.7 (45.8), 16 tokens 88 (97), 32 tokens 147 (130); one 4096 x
-// 4096 weight, 1 row 7.9 us (24.1), 12 rows 22.4 (24.0), 16 rows 28.5 (24.1).
-bool few_rows(const GroupedArgs& a) { return a.w_k == 1 && a.out_rows <= std::max(12, a.groups); }
+// Up to 8 rows, unless many weights have short rows, this kernel is the faster one (the matrix
+// unit's time in brackets, cold weights): one token's gate and up, hidden 2048 x 768 channels x
+// 128 experts top-8, 12.1 us (13.9), 8 bits 8.4 (9.6), but its 8-bit down product with k = 768 9.8
+// (6.7); one 4096 x 4096 bf16 weight, 1 row 7.9 us (19), 8 rows 16.4 (19), 12 rows 22.4 (19).
+bool few_rows(const GroupedArgs& a) {
+  const int64_t kbytes = (int64_t)a.k * (a.i8 ? 1 : 2);
+  const int64_t bytes = std::min(a.groups, a.out_rows) * (a.swiglu ? 2 : 1) * kbytes * a.n;
+  return a.w_k == 1 && a.out_rows <= 8 && (kbytes >= 1024 || bytes <= 1 << 20);
+}
 
 int launch_few(const GroupedArgs& a, const KArgs& k, cudaStream_t st) {
   if (a.swiglu) return a.i8 ? launch<true, true, false>(a, k, st) : launch<false, true, false>(a, k, st);
