@@ -122,6 +122,47 @@ def test_grouped_swiglu(msb, counts, n, k, record):
     within(msb.grouped_swiglu(x, w, offs, rows=rows), s * u, tol)
 
 
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("R,n,k", [(9, 100, 1000), (64, 640, 4096), (65, 300, 2050), (200, 1000, 1024), (3, 64, 20000)])
+def test_one_group_with_few_tiles(msb, R, n, k, gather):
+    """One weight and few rows: the tiles' k is shared out and joined.  Tolerances as above; 8-bit
+    sums stay exact."""
+    import torch
+    T = 40 if gather else R
+    rows = torch.randint(-1, T + 1, (R,), device="cuda", dtype=torch.int32) if gather else None
+    offs = offsets_of([R])
+    x = rnd(40, T, (k + 7) // 8 * 8)[:, :k]
+    for layout in ("k", "n"):
+        w = weight(41, 1, n, k, layout)
+        want, mag = product64(x, w, offs, rows)
+        for dtype, step in ((torch.bfloat16, BF16), (torch.float32, F32)):
+            got = msb.grouped_matmul(x, w, rows=rows, out_dtype=dtype)
+            within(got, want, step * want.abs() + k * 2 * F32 * mag + TINY, (layout, dtype))
+    w2 = weight(42, 2, n, k, "k")[None]
+    (g, ga), (u, ua) = (product64(x, w2[:, p], offs, rows) for p in range(2))
+    dg, du, sg = k * 2 * F32 * ga, k * 2 * F32 * ua, torch.nn.functional.silu(g)
+    tol = (BF16 + 2.0 ** -20) * (sg * u).abs() + 1.1 * dg * u.abs() + sg.abs() * du + 1.1 * dg * du + TINY
+    within(msb.grouped_swiglu(x, w2, rows=rows), sg * u, tol + 2.0 ** -117 * u.abs(), "swiglu")
+    gen = torch.Generator(device="cuda").manual_seed(43)
+    q = torch.randint(-128, 128, (T, (k + 15) // 16 * 16), device="cuda", generator=gen).to(torch.int8)[:, :k]
+    w8 = torch.randint(-128, 128, (n, (k + 15) // 16 * 16), device="cuda", generator=gen).to(torch.int8)[:, :k]
+    one, ones = torch.ones(T, device="cuda"), torch.ones(n, device="cuda")
+    want, _ = product64(q, w8[None], offs, rows)
+    within(msb.matmul_int8(q, one, w8, ones, rows=rows, out_dtype=torch.float32), want, F32 * want.abs())
+    within(msb.matmul_int8(q, one, w8, ones, rows=rows), want, (BF16 + F32) * want.abs())
+
+
+def test_float_outputs_keep_float_precision(msb):
+    """Float outputs at k = 8192: the sum is cut off every 256 k only, each time by less than 2^-23
+    of a part's size per addition; relative L2 below 1e-6 (the bf16 output's rounding is 2e-3)."""
+    import torch
+    for layout in ("k", "n"):
+        x, w = rnd(44, 500, 8192), weight(45, 1, 256, 8192, layout)
+        want, _ = product64(x, w, offsets_of([500]), None)
+        got = msb.grouped_matmul(x, w, out_dtype=torch.float32)
+        assert (got.double() - want).norm() < 1e-6 * want.norm()
+
+
 def test_swiglu_of_extreme_gates(msb):
     """Gates of +-300: silu is the gate itself and a zero of either sign, never NaN."""
     import torch

@@ -164,14 +164,34 @@ template <class Shared>
 __device__ __forceinline__ void release_acc(Shared& s, int buf, int lane) {
   tc_fence_before();
   __syncwarp();
-  if (lane == 0) arrive_pair(map_to(smem_addr(&s.acc_empty[buf]), 0));
+  if (lane == 0) arrive_pair(map_to(smem_addr(&s.acc_empty[buf]), cluster_rank() & ~1u));
+}
+
+// Parts of a tile from the cluster's other pairs (SPLIT > 1: every pair takes a range of k).
+// Each of their epilogue threads leaves its accumulator words in the stages of the first pair's
+// CTA of the same weight rows, which has finished with them: word j of part p (1 ..) of warp w.
+// All threads of the cluster meet twice, before the parts are written and before they are
+// read; `met` counts.
+__device__ __forceinline__ uint32_t part_offset(int part, int warp, int j, int lane) {
+  return ((((part - 1) * 4 + warp) * 64 + j) * 32 + lane) * 4;
+}
+__device__ __forceinline__ void meet(int& met) {
+  __syncwarp();
+  cluster_sync();
+  ++met;
+}
+template <bool I8>
+__device__ __forceinline__ uint32_t add_part(uint32_t v, const uint8_t* stages, int part, int warp, int j, int lane) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(stages + part_offset(part, warp, j, lane));
+  return I8 ? v + w : __float_as_uint(__uint_as_float(v) + __uint_as_float(w));
 }
 
 // One epilogue warp's 32 channels to float: a lane is a channel.  8-bit sums are exact; bf16
 // products come in parts of kExactStages stages, which are summed here.
-template <int BN, bool I8>
-__device__ __forceinline__ bool store_f32(const KArgs& a, typename Cfg<BN>::Shared& s, const Tile& tile, uint32_t tmem,
-                                          int& buf, uint32_t& phase, int nk, uint32_t rank, int warp, int lane) {
+template <int BN, bool I8, int SPLIT>
+__device__ __forceinline__ bool store_f32(const KArgs& a, typename Cfg<BN>::Shared& s, uint8_t* stages, const Tile& tile,
+                                          uint32_t tmem, int& buf, uint32_t& phase, int nk, uint32_t rank, int part,
+                                          int warp, int lane, int& met) {
   const int ch = tile.m * kTileM + (int)rank * 128 + warp * 32 + lane;
   float* const out = static_cast<float*>(a.out) + (int64_t)tile.row0 * a.ldo + ch;
   const uint32_t acc = tmem + ((uint32_t)(warp * 32) << 16);
@@ -179,11 +199,25 @@ __device__ __forceinline__ bool store_f32(const KArgs& a, typename Cfg<BN>::Shar
     const float ws = ch < a.n ? a.w_scale[(int64_t)tile.group * a.n + ch] : 0.f;
     if (!wait_warp(&s.acc_full[buf], phase, &s.dead)) return false;
     tc_fence_after();
+    if (SPLIT > 1) {
+      meet(met);
+      if (part == 0) meet(met);
+    }
     for (int c0 = 0; c0 < tile.rows; c0 += 32) {
       uint32_t v[32];
       tmem_ld32(acc + buf * BN + c0, v);
       tmem_ld_wait();
       if (c0 + 32 >= tile.rows) release_acc(s, buf, lane);
+      if (SPLIT > 1 && part > 0) {
+        const uint32_t to = map_to(smem_addr(stages), rank);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) store_cluster(to + part_offset(part, warp, c0 + c, lane), v[c]);
+        continue;
+      }
+      if (SPLIT > 1)
+        for (int q = 1; q < SPLIT; ++q)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = add_part<true>(v[c], stages, q, warp, c0 + c, lane);
       if (ch < a.n)
 #pragma unroll
         for (int c = 0; c < 32; ++c)
@@ -210,6 +244,20 @@ __device__ __forceinline__ bool store_f32(const KArgs& a, typename Cfg<BN>::Shar
       release_acc(s, buf, lane);
       if (++buf == 2) buf = 0, phase ^= 1;
     }
+    if (SPLIT > 1) {
+      meet(met);
+      if (part > 0) {
+        const uint32_t to = map_to(smem_addr(stages), rank);
+#pragma unroll
+        for (int c = 0; c < BN; ++c) store_cluster(to + part_offset(part, warp, c, lane), __float_as_uint(sum[c]));
+        return true;
+      }
+      meet(met);
+      for (int q = 1; q < SPLIT; ++q)
+#pragma unroll
+        for (int c = 0; c < BN; ++c)
+          sum[c] = __uint_as_float(add_part<false>(__float_as_uint(sum[c]), stages, q, warp, c, lane));
+    }
     if (ch < a.n)
 #pragma unroll
       for (int c = 0; c < BN; ++c)
@@ -222,9 +270,10 @@ __device__ __forceinline__ bool store_f32(const KArgs& a, typename Cfg<BN>::Shar
 // along the lanes of tensor memory and contiguously in the output, so 32 columns (rows of out)
 // at a time are turned through shared memory (transposing 8x8 stores) and leave as 16-byte
 // pieces; element by element where out is not aligned for that or the channels end.
-template <int BN, bool I8, bool GATED>
-__device__ __forceinline__ bool store_bf16(const KArgs& a, typename Cfg<BN>::Shared& s, const Tile& tile, uint32_t tmem, int buf,
-                                           uint32_t phase, uint32_t rank, int warp, int lane) {
+template <int BN, bool I8, bool GATED, int SPLIT>
+__device__ __forceinline__ bool store_bf16(const KArgs& a, typename Cfg<BN>::Shared& s, uint8_t* stages,
+                                           const Tile& tile, uint32_t tmem, int buf, uint32_t phase, uint32_t rank,
+                                           int part, int warp, int lane, int& met) {
   constexpr int kCh = GATED ? 16 : 32;  // channels of this warp
   const int ch0 = GATED ? tile.m * 128 + (int)rank * 64 + warp * 16 : tile.m * kTileM + (int)rank * 128 + warp * 32;
   // scales of the accumulator rows lane / 4 + 8 i
@@ -240,6 +289,10 @@ __device__ __forceinline__ bool store_bf16(const KArgs& a, typename Cfg<BN>::Sha
   }
   if (!wait_warp(&s.acc_full[buf], phase, &s.dead)) return false;
   tc_fence_after();
+  if (SPLIT > 1) {
+    meet(met);
+    if (part == 0) meet(met);
+  }
   const uint32_t acc = tmem + buf * BN + ((uint32_t)(warp * 32) << 16);
   uint8_t* const stage = s.out[warp];
   const int lim = a.n - ch0;  // channels of this warp that exist (may be <= 0)
@@ -249,6 +302,17 @@ __device__ __forceinline__ bool store_bf16(const KArgs& a, typename Cfg<BN>::Sha
     tmem_ld16(acc + (16u << 16) + c0, v[1]);
     tmem_ld_wait();
     if (c0 + 32 >= tile.rows) release_acc(s, buf, lane);
+    if (SPLIT > 1 && part > 0) {
+      const uint32_t to = map_to(smem_addr(stages), rank);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) store_cluster(to + part_offset(part, warp, c0 + j, lane), v[j >> 4][j & 15]);
+      continue;
+    }
+    if (SPLIT > 1)
+      for (int q = 1; q < SPLIT; ++q)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          v[j >> 4][j & 15] = add_part<I8>(v[j >> 4][j & 15], stages, q, warp, c0 + j, lane);
     __syncwarp();  // the last 32 rows have been read
     float2 rs[4];
 #pragma unroll
@@ -303,9 +367,10 @@ __device__ __forceinline__ bool store_bf16(const KArgs& a, typename Cfg<BN>::Sha
 }
 
 // I8: 8-bit integers (else bf16).  MMAJOR: the weight's n runs contiguously (bf16 only).
-// GATED: rows of the weight tile alternate in eights, gate and up.  F32: float output.
-template <int BN, bool I8, bool MMAJOR, bool GATED, bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1)
+// GATED: rows of the weight tile alternate in eights, gate and up.  F32: float output.  SPLIT:
+// pairs that share a tile's k (with one tile per cluster and BN = 64).
+template <int BN, bool I8, bool MMAJOR, bool GATED, bool F32, int SPLIT>
+__global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ RowMaps xmaps,
                    const KArgs a) {
   using C = Cfg<BN>;
@@ -315,9 +380,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
   uint8_t* const stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   auto& s = *reinterpret_cast<typename C::Shared*>(stages + (size_t)kStages * C::kStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int nk = (a.kbytes + kStageBytes - 1) / kStageBytes;
+  const uint32_t leader = cluster_rank() & ~1u, rank = cluster_rank() & 1;  // of the pair, in the pair
+  const int part = cluster_rank() >> 1;
+  const int pair = blockIdx.x / (2 * SPLIT), pairs = gridDim.x / (2 * SPLIT);  // of clusters, if they are larger
+  const int whole = (a.kbytes + kStageBytes - 1) / kStageBytes;
+  const int kb = SPLIT > 1 ? whole * part / SPLIT : 0;  // first stage of k here, and how many
+  const int nk = (SPLIT > 1 ? whole * (part + 1) / SPLIT : whole) - kb;
+  int met = 0;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) {
@@ -357,9 +426,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
       const uint32_t bytes = 2 * kABytes + (a.rows ? 0 : ((tile.rows + 31) & ~31) * kStageBytes);
       for (int i = 0; i < nk; ++i) {
         if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
-        const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
+        const uint32_t bar = map_to(smem_addr(&s.full[st]), leader);
         const uint32_t dst = smem_addr(stages) + st * C::kStage;
-        const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
+        const int k0 = (kb + i) * (I8 ? kStageBytes : kStageBytes / 2);
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
           if constexpr (GATED) {
@@ -404,13 +473,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
             for (int q = 0; q < 4; ++q)
               mma_pair<I8>(tmem + buf * BN, da + q * (MMAJOR ? 2048 >> 4 : 32 >> 4), db + q * (32 >> 4), idesc,
                            i > i0 || q > 0);
-            mma_commit_pair(&s.empty[st]);
+            mma_commit_pair(&s.empty[st], 3u << leader);
           }
           __syncwarp();
           if (++st == kStages) st = 0, phase ^= 1;
         }
         if (!ok) break;
-        if (elect_one()) mma_commit_pair(&s.acc_full[buf]);
+        if (elect_one()) mma_commit_pair(&s.acc_full[buf], 3u << leader);
         __syncwarp();
         if (++buf == 2) buf = 0, acc_phase ^= 1;
       }
@@ -419,7 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
     // ------------------------------------------------ rows of x, gathered
     const int st = (warp - 6) / kSplit, part = (warp - 6) % kSplit;
     const int chunk = lane & 7, r0 = lane >> 3;  // 16-byte piece of 128, row of each four
-    const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
+    const uint32_t bar = map_to(smem_addr(&s.full[st]), leader);
     const uint32_t base = smem_addr(stages) + st * C::kStage + kABytes + r0 * kStageBytes;
     uint32_t phase = 0;
     int at = 0;  // stages before this tile, modulo the ring
@@ -452,9 +521,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
       for (; i < nk; i += kStages) {
         if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
         phase ^= 1;
-        const int left = a.kbytes - i * kStageBytes - chunk * 16;
+        const int left = a.kbytes - (kb + i) * kStageBytes - chunk * 16;
         const uint32_t valid = left < 0 ? 0 : left > 16 ? 16 : left;
-        const int64_t k0 = valid ? (int64_t)i * kStageBytes : 0;
+        const int64_t k0 = valid ? (int64_t)(kb + i) * kStageBytes : 0;
 #pragma unroll
         for (int q = 0; q < C::kLaneRows; ++q)
           if (q * 4 < mine)
@@ -476,9 +545,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
       const int row0 = tile.row0 + (int)rank * half;
       for (int i = 0; i < nk; ++i) {
         if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
-        const uint32_t bar = map_to(smem_addr(&s.full[st]), 0);
+        const uint32_t bar = map_to(smem_addr(&s.full[st]), leader);
         const uint32_t dst = smem_addr(stages) + st * C::kStage + kABytes;
-        const int k0 = i * (I8 ? kStageBytes : kStageBytes / 2);
+        const int k0 = (kb + i) * (I8 ? kStageBytes : kStageBytes / 2);
         // rows behind the group's last belong to the next group: their columns of the
         // accumulator are not stored
         if (elect_one()) {
@@ -509,14 +578,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1
       }
       // the accumulator is handed back once it has been read, before the last stores
       if constexpr (F32) {
-        ok = store_f32<BN, I8>(a, s, tile, tmem, buf, acc_phase, nk, rank, warp, lane);
+        ok = store_f32<BN, I8, SPLIT>(a, s, stages, tile, tmem, buf, acc_phase, nk, rank, part, warp, lane, met);
       } else {
-        ok = store_bf16<BN, I8, GATED>(a, s, tile, tmem, buf, acc_phase, rank, warp, lane);
+        ok = store_bf16<BN, I8, GATED, SPLIT>(a, s, stages, tile, tmem, buf, acc_phase, rank, part, warp, lane, met);
         if (++buf == 2) buf = 0, acc_phase ^= 1;
       }
     }
   }
   __syncwarp();
+  if (SPLIT > 1)
+    while (met < 2) meet(met);
   // A role that gave up may leave copies or instructions in flight: they end within
   // microseconds; let them, so that none reaches an exited CTA or freed tensor memory.
   if (*(volatile uint32_t*)&s.dead) {
@@ -597,9 +668,9 @@ bool row_maps(const GroupedArgs& a, RowMaps* maps) {
   return true;
 }
 
-template <int BN, bool I8, bool MMAJOR, bool GATED, bool F32>
+template <int BN, bool I8, bool MMAJOR, bool GATED, bool F32, int SPLIT = 1>
 int launch(const CUtensorMap& map, const RowMaps& xmaps, const KArgs& k, cudaStream_t st) {
-  const auto kernel = grouped_kernel<BN, I8, MMAJOR, GATED, F32>;
+  const auto kernel = grouped_kernel<BN, I8, MMAJOR, GATED, F32, SPLIT>;
   struct Device {
     std::once_flag once;
     cudaError_t rc;
@@ -614,38 +685,82 @@ int launch(const CUtensorMap& map, const RowMaps& xmaps, const KArgs& k, cudaStr
     if (d.rc == cudaSuccess) d.rc = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
   });
   if (d.rc != cudaSuccess) return MSB_ECUDA;
-  // at most one pair per tile: pieces <= groups + rows / BN
+  // at most one pair (or cluster) per tile: pieces <= groups + rows / BN, and every piece has a row
   const int64_t most = ((int64_t)k.groups + k.out_rows / BN) * k.mtiles;
-  const int64_t mine = (int64_t)k.out_rows * k.mtiles;  // and every piece has a row
-  const int pairs = (int)std::min<int64_t>(d.sms / 2, std::min(most, mine));
-  return launch_early(kernel, 2 * pairs, Cfg<BN>::kThreads, Cfg<BN>::kSmemBytes, st, map, xmaps, k);
+  const int64_t mine = (int64_t)k.out_rows * k.mtiles;
+  const int64_t clusters = SPLIT > 1 ? (int64_t)(k.out_rows + BN - 1) / BN * k.mtiles
+                                     : std::min<int64_t>(d.sms / 2, std::min(most, mine));
+  return launch_early(kernel, 2 * SPLIT * clusters, Cfg<BN>::kThreads, Cfg<BN>::kSmemBytes, st, map, xmaps, k);
 }
 
-template <int BN>
+template <int BN, int SPLIT = 1>
 int launch_tile(const GroupedArgs& a, const CUtensorMap& map, const RowMaps& xmaps, const KArgs& k, cudaStream_t st) {
   if (a.i8) {
-    if (a.swiglu) return launch<BN, true, false, true, false>(map, xmaps, k, st);
-    return a.out_f32 ? launch<BN, true, false, false, true>(map, xmaps, k, st)
-                     : launch<BN, true, false, false, false>(map, xmaps, k, st);
+    if (a.swiglu) return launch<BN, true, false, true, false, SPLIT>(map, xmaps, k, st);
+    return a.out_f32 ? launch<BN, true, false, false, true, SPLIT>(map, xmaps, k, st)
+                     : launch<BN, true, false, false, false, SPLIT>(map, xmaps, k, st);
   }
-  if (a.swiglu) return launch<BN, false, false, true, false>(map, xmaps, k, st);
+  if (a.swiglu) return launch<BN, false, false, true, false, SPLIT>(map, xmaps, k, st);
   if constexpr (BN == 64)
     if (a.out_f32)
-      return a.w_k != 1 ? launch<BN, false, true, false, true>(map, xmaps, k, st)
-                        : launch<BN, false, false, false, true>(map, xmaps, k, st);
-  return a.w_k != 1 ? launch<BN, false, true, false, false>(map, xmaps, k, st)
-                    : launch<BN, false, false, false, false>(map, xmaps, k, st);
+      return a.w_k != 1 ? launch<BN, false, true, false, true, SPLIT>(map, xmaps, k, st)
+                        : launch<BN, false, false, false, true, SPLIT>(map, xmaps, k, st);
+  return a.w_k != 1 ? launch<BN, false, true, false, false, SPLIT>(map, xmaps, k, st)
+                    : launch<BN, false, false, false, false, SPLIT>(map, xmaps, k, st);
+}
+
+constexpr int kPairs = 74;  // CTA pairs that the device holds
+
+// Clusters of 2 * SPLIT CTAs that the current device holds at once (of any 64-row kernel: they
+// take the same shared memory and threads).
+template <int SPLIT>
+int resident_clusters() {
+  static std::mutex mu;
+  static int known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev] == 0) {
+    const auto kernel = grouped_kernel<64, false, false, false, false, SPLIT>;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2 * SPLIT, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * SPLIT * kPairs);
+    cfg.blockDim = dim3(Cfg<64>::kThreads);
+    cfg.dynamicSmemBytes = Cfg<64>::kSmemBytes;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<64>::kSmemBytes) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess)
+      n = 0;
+    known[dev] = n > 0 ? n : -1;
+  }
+  return known[dev];
+}
+
+// Pairs that share the k of each tile of 64 rows: one group whose tiles are so few that the
+// device holds all their clusters at once, and enough stages that the join (two meetings of the
+// cluster and the parts' way through shared memory, 2 us) pays.  Without and with it, 64 rows: a
+// bf16 weight of 4096 x 4096 16.9 and 13.3 us, 512 x 4096 15.9 and 10.1, but 1024 x 1024 (16
+// stages) 7.2 and 8.0.
+int split_k(const GroupedArgs& a, const KArgs& k) {
+  const int64_t tiles = ((int64_t)a.out_rows + 63) / 64 * k.mtiles, stages = (k.kbytes + kStageBytes - 1) / kStageBytes;
+  if (a.groups != 1 || stages < 32) return 1;
+  return tiles <= resident_clusters<4>() ? 4 : tiles <= resident_clusters<2>() ? 2 : 1;
 }
 
 // Rows of the tile that serves a product.
 int tile_rows(const GroupedArgs& a, const KArgs& k) {
   if (a.out_f32 && !a.i8) return 64;  // sums in registers
-  const int64_t rows = a.out_rows, pairs = 74, groups = std::min<int64_t>(a.groups, rows);
+  const int64_t rows = a.out_rows, groups = std::min<int64_t>(a.groups, rows);
   // Few tiles: the smallest that one round of the pairs holds (one 4096 x 4096 bf16 weight, 64-,
   // 128- and 256-row tiles: 256 rows 19.0, 19.8, 26.4 us; 512 rows 31.9, 20.0, 27.4; 1024 rows
   // 57, 34, 28).
   for (int bn = 64; bn <= 256; bn *= 2)
-    if (k.mtiles * std::max(groups, (rows + bn - 1) / bn) <= pairs) return bn;
+    if (k.mtiles * std::max(groups, (rows + bn - 1) / bn) <= kPairs) return bn;
   // Many: by the rows of a group, on average (gate and up of hidden 2048 x 768 channels x 128
   // experts; bf16, 32 rows 131, 129, 137 us; 64 rows 176, 148, 147; 128 rows 256, 199, 167; 8
   // bits, 16 rows 67, 75, 94; 64 rows 91, 88, 128; 128 rows 137, 120, 125).
@@ -660,6 +775,10 @@ int launch_grouped(const GroupedArgs& a, cudaStream_t st) {
   CUtensorMap map;
   RowMaps xmaps = {};
   if (!weight_map(a, &map) || !row_maps(a, &xmaps)) return MSB_ECUDA;
+  switch (split_k(a, k)) {
+    case 4: return launch_tile<64, 4>(a, map, xmaps, k, st);
+    case 2: return launch_tile<64, 2>(a, map, xmaps, k, st);
+  }
   switch (tile_rows(a, k)) {
     case 64: return launch_tile<64>(a, map, xmaps, k, st);
     case 128: return launch_tile<128>(a, map, xmaps, k, st);

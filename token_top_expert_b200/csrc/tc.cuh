@@ -44,13 +44,13 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b
         : "memory");
 }
 
-// Arrive on `bar` of both CTAs of the pair once the matrix instructions issued so far by this
+// Arrive on `bar` of both CTAs of the pair (bits of their cluster ranks in `pair`) once the matrix instructions issued so far by this
 // thread have completed (and no longer read shared memory).
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t pair) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
       "[%0], %1;" ::"r"(smem_addr(bar)),
-      "h"((uint16_t)3)
+      "h"((uint16_t)pair)
       : "memory");
 }
 
@@ -179,6 +179,9 @@ __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
 // also wait for the thread's stores to global memory: about 2100 cycles here.)
 __device__ __forceinline__ void arrive_pair(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
