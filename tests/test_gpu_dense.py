@@ -175,6 +175,37 @@ def test_swiglu_of_extreme_gates(msb):
     assert torch.equal(h[1], torch.zeros(3, device="cuda"))
 
 
+@pytest.mark.parametrize("R", [1, 2, 3, 4, 5, 7, 8])
+@pytest.mark.parametrize("k", [8, 33, 520, 2056, 4100])
+def test_few_rows(msb, R, k):
+    """Single tokens: rows of several groups and of one, indices outside x among them."""
+    import torch
+    n, T = 71, 5
+    x = rnd(50, T, (k + 7) // 8 * 8)[:, :k]
+    rows = torch.randint(-1, T + 1, (R,), device="cuda", dtype=torch.int32)
+    for counts in ([R], [0, R // 2, 0, R - R // 2, 0]):
+        offs, E = offsets_of(counts), len(counts)
+        w = weight(51, 2 * E, n, k, "k").unflatten(0, (E, 2))
+        want, mag = product64(x, w[:, 0], offs, rows)
+        for dtype, step in ((torch.bfloat16, BF16), (torch.float32, F32)):
+            got = msb.grouped_matmul(x, w[:, 0], offs, rows=rows, out_dtype=dtype)
+            within(got, want, step * want.abs() + k * 2 * F32 * mag + TINY, dtype)
+        u, ua = product64(x, w[:, 1], offs, rows)
+        s = torch.nn.functional.silu(want)
+        dg, du = k * 2 * F32 * mag, k * 2 * F32 * ua
+        tol = (BF16 + 2.0 ** -20) * (s * u).abs() + 1.1 * dg * u.abs() + s.abs() * du + 1.1 * dg * du + TINY
+        within(msb.grouped_swiglu(x, w, offs, rows=rows), s * u, tol + 2.0 ** -117 * u.abs(), "swiglu")
+        q, qs = msb.quantize_int8(x)
+        w8 = torch.randint(-127, 128, (E, n, (k + 15) // 16 * 16), device="cuda").to(torch.int8)[..., :k]
+        ws = rnd(52, E, n, dtype=torch.float32)
+        want = product64(q, w8, offs, rows)[0]
+        ok = (rows >= 0) & (rows < T)
+        want = want * torch.where(ok, qs[rows.long().clamp(0, T - 1)], 0.0).double()[:, None]
+        for e, (lo, hi) in enumerate(zip(offs.tolist(), offs.tolist()[1:])):
+            want[lo:hi] *= ws[e].double()
+        within(msb.matmul_int8(q, qs, w8, ws, offs, rows=rows), want, (BF16 + 3.1 * F32) * want.abs() + TINY, "int8")
+
+
 def test_rows_of_no_group_and_bad_indices(msb):
     """Rows before the first offset, behind the last and spare rows of out stay as they were; a
     row index outside x reads zeros; offsets out of order or out of range touch nothing else."""
@@ -191,9 +222,10 @@ def test_rows_of_no_group_and_bad_indices(msb):
     assert (out[:7] == 7).all() and (out[32:] == 7).all()
     assert (out[9] == 0).all() and (out[12] == 0).all() and (out[13] == 0).all()
     for bad in ([-5, 3, 2, 1000], [2 ** 31 - 1, 0, -2 ** 31, 4], [40, 30, 20, 10]):
-        out.fill_(7.0)
-        msb.grouped_matmul(x, w, torch.tensor(bad, dtype=torch.int32, device="cuda"), rows=rows, out=out)
-        assert (out[40:] == 7).all()
+        for R in (40, 6):
+            out.fill_(7.0)
+            msb.grouped_matmul(x, w, torch.tensor(bad, dtype=torch.int32, device="cuda"), rows=rows[:R], out=out)
+            assert (out[R:] == 7).all()
 
 
 def test_wide_pitches_and_strided_views(msb):
@@ -239,7 +271,8 @@ def test_output_offsets_pass_32_bits(msb):
 # ------------------------------------------------------------------ 8 bits
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
-@pytest.mark.parametrize("R,k", [(1, 1), (3, 17), (70, 256), (5, 5000), (2, 20000)])
+@pytest.mark.parametrize("R,k", [(1, 1), (3, 17), (70, 256), (5, 5000), (2, 20000), (1300, 1032), (1201, 2048),
+                                 (1185, 4096)])
 def test_quantize_int8(msb, R, k, dtype):
     """Bit for bit the stated float32 steps."""
     import torch

@@ -381,7 +381,7 @@ int32_t msb_block_norm(const void* h, int32_t h_type, int64_t ldh, const void* y
   a.ldh = ldh, a.ldy = ldy, a.ldh_out = ldh_out, a.ldx = ldx, a.gate_row = gate_row, a.gate_col = gate_col;
   a.rows = rows, a.d = d, a.h_f32 = h_type == MSB_F32, a.y_f32 = y_type == MSB_F32, a.w_f32 = weight_type == MSB_F32;
   a.gate_f32 = gate_type == MSB_F32, a.post_norm = post_norm != 0;
-  a.skip = skip_scale, a.residual = residual_scale, a.eps = eps;
+  a.skip = skip_scale, a.residual = residual_scale, a.eps = eps, a.inv_d = 1.f / (float)d;
   return launch_block_norm(a, static_cast<cudaStream_t>(stream));
 }
 

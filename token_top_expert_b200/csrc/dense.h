@@ -44,7 +44,7 @@ struct NormArgs {
   int64_t ldh, ldy, ldh_out, ldx, gate_row, gate_col;
   int rows, d;
   bool h_f32, y_f32, w_f32, gate_f32, post_norm;
-  float skip, residual, eps;
+  float skip, residual, eps, inv_d;
 };
 int launch_block_norm(const NormArgs& a, cudaStream_t st);
 

@@ -17,7 +17,9 @@ __device__ __forceinline__ float load(const void* p, bool f32, int64_t i) {
 }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  return (uint32_t)bf16_bits(lo) | (uint32_t)bf16_bits(hi) << 16;
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // W consecutive elements (8: the address is 16-byte aligned).
@@ -58,13 +60,10 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   if constexpr (NT > 32) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    if constexpr (NT > 256) {
-      v = warp_sum((threadIdx.x & 31) < NT / 32 ? red[threadIdx.x & 31] : 0.f);
-    } else {
-      v = 0.f;
+    const float4* const r4 = reinterpret_cast<const float4*>(red);
+    v = 0.f;
 #pragma unroll
-      for (int w = 0; w < NT / 32; ++w) v += red[w];
-    }
+    for (int w = 0; w < NT / 128; ++w) v += (r4[w].x + r4[w].y) + (r4[w].z + r4[w].w);
   }
   return v;
 }
@@ -82,6 +81,27 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
 
 __host__ __device__ constexpr int block_threads(int nt) { return nt == 32 ? 256 : nt; }
 
+// Eight elements as they lie in memory.
+template <bool F32>
+struct Raw {
+  uint4 a[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const uint4* const q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * (F32 ? 4 : 2));
+#pragma unroll
+    for (int j = 0; j < (F32 ? 2 : 1); ++j) a[j] = q[j];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if constexpr (F32) {
+      v[0] = __uint_as_float(a[0].x), v[1] = __uint_as_float(a[0].y), v[2] = __uint_as_float(a[0].z);
+      v[3] = __uint_as_float(a[0].w), v[4] = __uint_as_float(a[1].x), v[5] = __uint_as_float(a[1].y);
+      v[6] = __uint_as_float(a[1].z), v[7] = __uint_as_float(a[1].w);
+    } else {
+      v[0] = bf16_lo(a[0].x), v[1] = bf16_hi(a[0].x), v[2] = bf16_lo(a[0].y), v[3] = bf16_hi(a[0].y);
+      v[4] = bf16_lo(a[0].z), v[5] = bf16_hi(a[0].z), v[6] = bf16_lo(a[0].w), v[7] = bf16_hi(a[0].w);
+    }
+  }
+};
+
 // ------------------------------------------------------------------ 8-bit quantisation
 
 struct QuantScale {
@@ -93,7 +113,15 @@ __device__ __forceinline__ QuantScale quant_scale(uint32_t big) {
   if (most < 1.504632769e-36f) return {0.f, 0.f};                      // below 2^-119
   return {most / 127.f, 127.f / most};
 }
-__device__ __forceinline__ int32_t quant(float v, float inv) { return inv == 0.f ? 0 : __float2int_rn(v * inv); }
+// The integer nearest to v * inv (at most 127 in magnitude), ties to even, in the low byte: adding
+// 1.5 * 2^23 rounds the product to a whole number and leaves it in the low bits of the sum.
+__device__ __forceinline__ uint32_t quant(float v, float inv) {
+  return __float_as_uint(__fadd_rn(__fmul_rn(v, inv), 12582912.f));
+}
+__device__ __forceinline__ uint32_t quant4(const float* v, float inv) {
+  return __byte_perm(__byte_perm(quant(v[0], inv), quant(v[1], inv), 0x0040),
+                     __byte_perm(quant(v[2], inv), quant(v[3], inv), 0x0040), 0x5410);
+}
 
 // V pieces of W elements a thread.
 template <int NT, int W, int V>
@@ -120,22 +148,55 @@ __global__ void __launch_bounds__(block_threads(NT))
       for (int c = 0; c < W; ++c) big = max(big, __float_as_uint(v[j][c]) & 0x7fffffffu);
   const QuantScale qs = quant_scale(row_max<NT>(big, red));
   if (tid == 0) scale[row] = qs.scale;
+  const bool zero = qs.inv == 0.f;  // nothing to scale, or not finite
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int i = (j * NT + tid) * W;
     if (i >= k) continue;
     int8_t* const o = q + row * ldq + i;
     if constexpr (W == 1) {
-      *o = (int8_t)quant(v[j][0], qs.inv);
+      *o = zero ? 0 : (int8_t)quant(v[j][0], qs.inv);
     } else {
-      uint32_t lo = 0, hi = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        lo |= (uint32_t)(uint8_t)quant(v[j][c], qs.inv) << (8 * c);
-        hi |= (uint32_t)(uint8_t)quant(v[j][c + 4], qs.inv) << (8 * c);
-      }
-      *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
+      *reinterpret_cast<uint2*>(o) =
+          zero ? make_uint2(0, 0) : make_uint2(quant4(&v[j][0], qs.inv), quant4(&v[j][4], qs.inv));
     }
+  }
+}
+
+// Many rows: a warp to a row, V pieces of eight elements a lane, all on their way at once (8192 x
+// 4096: 19.2 us, 5.2 TB/s, where a block per row takes 24).
+template <int V, bool F32>
+__global__ void __launch_bounds__(256) quantize_warp_kernel(const void* x, int64_t ldx, int rows, int k, int8_t* q,
+                                                            int64_t ldq, float* scale) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 31;
+  Raw<F32> r[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if ((j * 32 + lane) * 8 < k) r[j].load(x, row * ldx + (j * 32 + lane) * 8);
+  uint32_t big = 0;
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if ((j * 32 + lane) * 8 < k) {
+      float v[8];
+      r[j].get(v);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) big = max(big, __float_as_uint(v[c]) & 0x7fffffffu);
+    }
+  const QuantScale qs = quant_scale(__reduce_max_sync(0xffffffffu, big));
+  if (lane == 0) scale[row] = qs.scale;
+  const bool zero = qs.inv == 0.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int i = (j * 32 + lane) * 8;
+    if (i >= k) continue;
+    float v[8];
+    r[j].get(v);
+    *reinterpret_cast<uint2*>(q + row * ldq + i) =
+        zero ? make_uint2(0, 0) : make_uint2(quant4(v, qs.inv), quant4(v + 4, qs.inv));
   }
 }
 
@@ -150,29 +211,9 @@ __global__ void __launch_bounds__(256)
   for (int i = threadIdx.x; i < k; i += 256) big = max(big, __float_as_uint(load(x, f32, row * ldx + i)) & 0x7fffffffu);
   const QuantScale qs = quant_scale(row_max<256>(big, red));
   if (threadIdx.x == 0) scale[row] = qs.scale;
-  for (int i = threadIdx.x; i < k; i += 256) q[row * ldq + i] = (int8_t)quant(load(x, f32, row * ldx + i), qs.inv);
+  for (int i = threadIdx.x; i < k; i += 256)
+    q[row * ldq + i] = qs.inv == 0.f ? 0 : (int8_t)quant(load(x, f32, row * ldx + i), qs.inv);
 }
-
-// Eight elements as they lie in memory.
-template <bool F32>
-struct Raw {
-  uint4 a[F32 ? 2 : 1];
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-    const uint4* const q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + i * (F32 ? 4 : 2));
-#pragma unroll
-    for (int j = 0; j < (F32 ? 2 : 1); ++j) a[j] = q[j];
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    if constexpr (F32) {
-      v[0] = __uint_as_float(a[0].x), v[1] = __uint_as_float(a[0].y), v[2] = __uint_as_float(a[0].z);
-      v[3] = __uint_as_float(a[0].w), v[4] = __uint_as_float(a[1].x), v[5] = __uint_as_float(a[1].y);
-      v[6] = __uint_as_float(a[1].z), v[7] = __uint_as_float(a[1].w);
-    } else {
-      v[0] = bf16_lo(a[0].x), v[1] = bf16_hi(a[0].x), v[2] = bf16_lo(a[0].y), v[3] = bf16_hi(a[0].y);
-      v[4] = bf16_lo(a[0].z), v[5] = bf16_hi(a[0].z), v[6] = bf16_lo(a[0].w), v[7] = bf16_hi(a[0].w);
-    }
-  }
-};
 
 // ------------------------------------------------------------------ combine
 
@@ -259,14 +300,20 @@ __device__ __forceinline__ void branch(const NormArgs& a, int64_t t, int i, floa
   for (int c = 0; c < W; ++c) b[c] *= m[c];
 }
 
+// Blocks of an SM that the registers are cut to: more keep more loads in flight, fewer do not
+// spill (8192 x 4096, 4 and 3 blocks: bf16 48.5 and 51.4 us, float h 75.7 and 64.8; 8192 x 2048,
+// 6 and 4 blocks: 37.1 and 29.2).
+template <int NT, int V, bool F32>
+constexpr int kNormBlocks = (V == 4 ? 2 : V == 2 && F32 ? 3 : 4) * 256 / block_threads(NT);
+
 // b = [rms](y), h' = skip h + residual gate b, x = rms(h'), rows in 16-byte pieces.  The blocks
 // stay and take row after row: while a row's two sums cross the block, the next row's pieces
-// are on their way (without that the loads of a row wait for the row before: 77 us instead of
-// 46 us for 8192 x 4096 bf16, 268 MB).
+// are on their way.  8192 x 4096 bf16: 48.5 us, 5.5 TB/s (77 us with a block per row), where the
+// issue slots are three quarters full.
 template <int NT, int V, bool HF32, bool YF32>
-__global__ void __launch_bounds__(block_threads(NT)) block_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(block_threads(NT), kNormBlocks<NT, V, HF32 || YF32>) block_norm_kernel(const NormArgs a) {
   constexpr int kRows = block_threads(NT) / NT;
-  __shared__ float red[2][2][NT / 32];
+  alignas(16) __shared__ float red[2][2][NT / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x % NT;
@@ -302,7 +349,7 @@ __global__ void __launch_bounds__(block_threads(NT)) block_norm_kernel(const Nor
 #pragma unroll
           for (int c = 0; c < 8; ++c) ss = fmaf(y[c], y[c], ss);
         }
-      yscale = 1.f / sqrtf(row_sum<NT>(ss, red[turn][0]) / (float)a.d + a.eps);
+      yscale = rsqrtf(fmaf(row_sum<NT>(ss, red[turn][0]), a.inv_d, a.eps));
     }
     float h[V][8], ss = 0.f;
 #pragma unroll
@@ -324,7 +371,7 @@ __global__ void __launch_bounds__(block_threads(NT)) block_norm_kernel(const Nor
       if (a.h_out) store_w<8>(a.h_out, HF32, t * a.ldh_out + i, h[j]);
     }
     if (!a.x) continue;
-    const float inv = 1.f / sqrtf(row_sum<NT>(ss, red[turn][1]) / (float)a.d + a.eps);
+    const float inv = rsqrtf(fmaf(row_sum<NT>(ss, red[turn][1]), a.inv_d, a.eps));
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int i = (j * NT + tid) * 8;
@@ -342,55 +389,85 @@ __global__ void __launch_bounds__(block_threads(NT)) block_norm_kernel(const Nor
   }
 }
 
+// An element of a row that starts at p, of either type.
+__device__ __forceinline__ float at(const uint8_t* p, bool f32, int i) {
+  return f32 ? reinterpret_cast<const float*>(p)[i] : bf16_lo(reinterpret_cast<const uint16_t*>(p)[i]);
+}
+__device__ __forceinline__ const uint8_t* from(const void* p, bool f32, int64_t i) {
+  return p ? static_cast<const uint8_t*>(p) + i * (f32 ? 4 : 2) : nullptr;
+}
+
 // The same element by element, for rows that are not aligned in eights.
-template <int NT, int V>
+template <int NT, int V, bool HF32, bool YF32>
 __global__ void __launch_bounds__(block_threads(NT)) block_norm_any_kernel(const NormArgs a) {
-  __shared__ float red[2][NT / 32];
+  alignas(16) __shared__ float red[2][NT / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t t = (int64_t)blockIdx.x * (block_threads(NT) / NT) + threadIdx.x / NT;
   if (t >= a.rows) return;  // whole warps; larger rows have a block each
-  const int tid = threadIdx.x % NT;
+  const int tid = threadIdx.x % NT, here = a.d - tid;  // elements j * NT < here are this thread's
+  const uint8_t* const hp = from(a.h, HF32, t * a.ldh + tid);
+  const uint8_t* const yp = from(a.y, YF32, t * a.ldy + tid);
   float h[V], y[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int i = j * NT + tid;
-    y[j] = a.y && i < a.d ? load(a.y, a.y_f32, t * a.ldy + i) : 0.f;
-    h[j] = i < a.d ? load(a.h, a.h_f32, t * a.ldh + i) : 0.f;
+    y[j] = yp && j * NT < here ? at(yp, YF32, j * NT) : 0.f;
+    h[j] = j * NT < here ? at(hp, HF32, j * NT) : 0.f;
   }
-  float yscale = 1.f;
-  if (a.post_norm) {
-    float ss = 0.f;
+  if (yp) {
+    if (a.post_norm) {
+      float ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) ss = fmaf(y[j], y[j], ss);
-    yscale = 1.f / sqrtf(row_sum<NT>(ss, red[0]) / (float)a.d + a.eps);
+      for (int j = 0; j < V; ++j) ss = fmaf(y[j], y[j], ss);
+      const float yscale = rsqrtf(fmaf(row_sum<NT>(ss, red[0]), a.inv_d, a.eps));
+#pragma unroll
+      for (int j = 0; j < V; ++j) y[j] *= yscale;
+    }
+    if (const uint8_t* const w = from(a.post, a.w_f32, tid)) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (j * NT < here) y[j] *= at(w, a.w_f32, j * NT);
+    }
+    if (a.gate && a.gate_col == 0) {
+      const float g = load(a.gate, a.gate_f32, t * a.gate_row);
+#pragma unroll
+      for (int j = 0; j < V; ++j) y[j] *= g;
+    } else if (a.gate) {
+      const uint8_t* const g = from(a.gate, a.gate_f32, t * a.gate_row + tid * a.gate_col);
+      const int step = NT * (int)a.gate_col;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (j * NT < here) y[j] *= a.gate_col == 1 ? at(g, a.gate_f32, j * NT) : load(g, a.gate_f32, (int64_t)j * step);
+    }
   }
   float ss = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int i = j * NT + tid;
-    if (i >= a.d) continue;
-    h[j] *= a.skip;
-    if (a.y) {
-      float b[1] = {y[j]};
-      branch<1>(a, t, i, yscale, b);
-      h[j] = fmaf(a.residual, b[0], h[j]);
-    }
+    h[j] = fmaf(a.residual, y[j], a.skip * h[j]);
     ss = fmaf(h[j], h[j], ss);
-    if (a.h_out) {
-      const float v[1] = {h[j]};
-      store_w<1>(a.h_out, a.h_f32, t * a.ldh_out + i, v);
-    }
+  }
+  if (a.h_out) {
+    uint8_t* const o = const_cast<uint8_t*>(from(a.h_out, HF32, t * a.ldh_out + tid));
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j * NT < here) {
+        if constexpr (HF32) reinterpret_cast<float*>(o)[j * NT] = h[j];
+        else reinterpret_cast<uint16_t*>(o)[j * NT] = bf16_bits(h[j]);
+      }
   }
   if (!a.x) return;
-  const float inv = 1.f / sqrtf(row_sum<NT>(ss, red[1]) / (float)a.d + a.eps);
+  const float inv = rsqrtf(fmaf(row_sum<NT>(ss, red[1]), a.inv_d, a.eps));
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int i = j * NT + tid;
-    if (i >= a.d) continue;
-    const float v = h[j] * inv;
-    a.x[t * a.ldx + i] = bf16_bits(a.pre ? v * load(a.pre, a.w_f32, i) : v);
+  for (int j = 0; j < V; ++j) h[j] *= inv;
+  if (const uint8_t* const w = from(a.pre, a.w_f32, tid)) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j * NT < here) h[j] *= at(w, a.w_f32, j * NT);
   }
+  uint16_t* const o = a.x + t * a.ldx + tid;
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (j * NT < here) o[j * NT] = bf16_bits(h[j]);
 }
 
 // Blocks of a kernel that the current device holds at once.
@@ -406,6 +483,8 @@ int resident() {
     blocks[dev] = sms * per;
   return blocks[dev] > 0 ? blocks[dev] : 148;
 }
+
+constexpr int kManyRows = 148 * 8;  // rows from which a warp per row fills the device
 
 // Rows whose eights of elements are 16-byte aligned (a null pointer is).
 bool by8(const void* p, int64_t pitch, int64_t rows) {
@@ -426,7 +505,10 @@ int norm_rows(const NormArgs& a, cudaStream_t st) {
     if (a.h_f32) return a.y_f32 ? norm_wide<NT, V, true, true>(a, st) : norm_wide<NT, V, true, false>(a, st);
     return a.y_f32 ? norm_wide<NT, V, false, true>(a, st) : norm_wide<NT, V, false, false>(a, st);
   } else {
-    return launch_early(block_norm_any_kernel<NT, V>, ((int64_t)a.rows * NT + threads - 1) / threads, threads, 0, st, a);
+    const auto kernel = a.h_f32 ? (a.y_f32 ? block_norm_any_kernel<NT, V, true, true> : block_norm_any_kernel<NT, V, true, false>)
+                                : (a.y_f32 ? block_norm_any_kernel<NT, V, false, true>
+                                           : block_norm_any_kernel<NT, V, false, false>);
+    return launch_early(kernel, ((int64_t)a.rows * NT + threads - 1) / threads, threads, 0, st, a);
   }
 }
 
@@ -454,6 +536,11 @@ int launch_quantize(const void* x, bool f32, int64_t ldx, int rows, int k, int8_
                     float* scale, cudaStream_t st) {
   const bool wide = k % 8 == 0 && by8(x, ldx, rows) && reinterpret_cast<uintptr_t>(q) % 8 == 0 &&
                     (rows == 1 || ldq % 8 == 0);
+  if (wide && rows >= kManyRows && k > 1024 && k <= (f32 ? 2048 : 4096)) {
+    const auto kernel = f32 ? quantize_warp_kernel<8, true>
+                        : k <= 2048 ? quantize_warp_kernel<8, false> : quantize_warp_kernel<16, false>;
+    return launch_early(kernel, ((int64_t)rows + 7) / 8, 256, 0, st, x, ldx, rows, k, q, ldq, scale);
+  }
 #define MSB_QUANT(NT, W, V)                                                                          \
   launch_early(quantize_kernel<NT, W, V>, ((int64_t)rows * NT + block_threads(NT) - 1) / block_threads(NT), \
          block_threads(NT), 0, st, x, f32, ldx, rows, k, q, ldq, scale)
