@@ -419,17 +419,17 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(Cfg<BN>::kTh
 
   if (warp == 5) {
     // ------------------------------------------------ weights
-    int st = 0;
-    uint32_t phase = 0;
-    for (int t = pair; ok && t < tiles; t += pairs) {
-      const Tile tile = tile_at(a, s, t);
-      const uint32_t bytes = 2 * kABytes + (a.rows ? 0 : ((tile.rows + 31) & ~31) * kStageBytes);
-      for (int i = 0; i < nk; ++i) {
-        if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
-        const uint32_t bar = map_to(smem_addr(&s.full[st]), leader);
-        const uint32_t dst = smem_addr(stages) + st * C::kStage;
-        const int k0 = (kb + i) * (I8 ? kStageBytes : kStageBytes / 2);
-        if (elect_one()) {
+    if (elect_one()) {
+      const uint32_t base = smem_addr(stages), bars = map_to(smem_addr(&s.full[0]), leader);
+      int st = 0;
+      uint32_t phase = 0;
+      for (int t = pair; ok && t < tiles; t += pairs) {
+        const Tile tile = tile_at(a, s, t);
+        const uint32_t bytes = 2 * kABytes + (a.rows ? 0 : ((tile.rows + 31) & ~31) * kStageBytes);
+        int k0 = kb * (I8 ? kStageBytes : kStageBytes / 2);
+        for (int i = 0; i < nk; ++i, k0 += I8 ? kStageBytes : kStageBytes / 2) {
+          if (!(ok = wait_one(&s.empty[st], phase ^ 1, &s.dead))) break;
+          const uint32_t bar = bars + st * 8, dst = base + st * C::kStage;
           if (rank == 0) mbar_arrive_expect_tx(&s.full[st], bytes);
           if constexpr (GATED) {
             // eight channels' gate rows, then their up rows: 16 rows of the tile
@@ -445,43 +445,42 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(Cfg<BN>::kTh
           } else {
             tma_load_3d(dst, &wmap, k0, tile.m * kTileM + (int)rank * 128, tile.group, bar);
           }
+          if (++st == kStages) st = 0, phase ^= 1;
         }
-        __syncwarp();
-        if (++st == kStages) st = 0, phase ^= 1;
       }
     }
   } else if (warp == 4 && rank == 0) {
     // ------------------------------------------------ matrix instructions of the pair
-    int st = 0, buf = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    const int chunk = kExact<I8, F32> ? kExactStages : nk;  // stages summed in one accumulator
-    for (int t = pair; ok && t < tiles; t += pairs) {
-      const Tile tile = tile_at(a, s, t);
-      const uint32_t idesc = instr_desc(I8 ? 2 : 1, MMAJOR, kTileM, (tile.rows + 31) & ~31);
-      for (int i0 = 0; ok && i0 < nk; i0 += chunk) {
-        if (!(ok = wait_warp(&s.acc_empty[buf], acc_phase ^ 1, &s.dead))) break;
-        tc_fence_after();
-        for (int i = i0; i < min(i0 + chunk, nk); ++i) {
-          if (!(ok = wait_warp(&s.full[st], phase, &s.dead))) break;
+    if (elect_one()) {
+      int st = 0, buf = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      const int chunk = kExact<I8, F32> ? kExactStages : nk;  // stages summed in one accumulator
+      const uint32_t pa = smem_addr(stages);
+      const uint64_t da0 = MMAJOR ? smem_desc(pa, kABytes / 2, 1024) : smem_desc(pa, 16, 1024);
+      const uint64_t db0 = smem_desc(pa + kABytes, 16, 1024);
+      for (int t = pair; ok && t < tiles; t += pairs) {
+        const Tile tile = tile_at(a, s, t);
+        const uint32_t idesc = instr_desc(I8 ? 2 : 1, MMAJOR, kTileM, (tile.rows + 31) & ~31);
+        for (int i0 = 0; ok && i0 < nk; i0 += chunk) {
+          if (!(ok = wait_one(&s.acc_empty[buf], acc_phase ^ 1, &s.dead))) break;
           tc_fence_after();
-          const uint32_t pa = smem_addr(stages) + st * C::kStage;
-          const uint64_t da = MMAJOR ? smem_desc(pa, kABytes / 2, 1024) : smem_desc(pa, 16, 1024);
-          const uint64_t db = smem_desc(pa + kABytes, 16, 1024);
-          if (elect_one()) {
+          const int i1 = min(i0 + chunk, nk);
+          for (int i = i0; i < i1; ++i) {
+            if (!(ok = wait_one(&s.full[st], phase, &s.dead))) break;
+            tc_fence_after();
+            const uint64_t da = da0 + st * (C::kStage >> 4), db = db0 + st * (C::kStage >> 4);
             // steps of 32 bytes of k; m-major: of 16 rows
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               mma_pair<I8>(tmem + buf * BN, da + q * (MMAJOR ? 2048 >> 4 : 32 >> 4), db + q * (32 >> 4), idesc,
                            i > i0 || q > 0);
             mma_commit_pair(&s.empty[st], 3u << leader);
+            if (++st == kStages) st = 0, phase ^= 1;
           }
-          __syncwarp();
-          if (++st == kStages) st = 0, phase ^= 1;
+          if (!ok) break;
+          mma_commit_pair(&s.acc_full[buf], 3u << leader);
+          if (++buf == 2) buf = 0, acc_phase ^= 1;
         }
-        if (!ok) break;
-        if (elect_one()) mma_commit_pair(&s.acc_full[buf], 3u << leader);
-        __syncwarp();
-        if (++buf == 2) buf = 0, acc_phase ^= 1;
       }
     }
   } else if (warp >= 6 && a.rows) {
@@ -537,29 +536,27 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(Cfg<BN>::kTh
     }
   } else if (warp == 6 && !a.rows) {
     // ------------------------------------------------ rows of x, as they lie
-    int st = 0;
-    uint32_t phase = 0;
-    for (int t = pair; ok && t < tiles; t += pairs) {
-      const Tile tile = tile_at(a, s, t);
-      const int half = ((tile.rows + 31) & ~31) >> 1;
-      const int row0 = tile.row0 + (int)rank * half;
-      for (int i = 0; i < nk; ++i) {
-        if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
-        const uint32_t bar = map_to(smem_addr(&s.full[st]), leader);
-        const uint32_t dst = smem_addr(stages) + st * C::kStage + kABytes;
-        const int k0 = (kb + i) * (I8 ? kStageBytes : kStageBytes / 2);
-        // rows behind the group's last belong to the next group: their columns of the
-        // accumulator are not stored
-        if (elect_one()) {
+    if (elect_one()) {
+      const uint32_t base = smem_addr(stages) + kABytes, bars = map_to(smem_addr(&s.full[0]), leader);
+      int st = 0;
+      uint32_t phase = 0;
+      for (int t = pair; ok && t < tiles; t += pairs) {
+        const Tile tile = tile_at(a, s, t);
+        const int half = ((tile.rows + 31) & ~31) >> 1;
+        const int row0 = tile.row0 + (int)rank * half;
+        int k0 = kb * (I8 ? kStageBytes : kStageBytes / 2);
+        for (int i = 0; i < nk; ++i, k0 += I8 ? kStageBytes : kStageBytes / 2) {
+          if (!(ok = wait_one(&s.empty[st], phase ^ 1, &s.dead))) break;
+          // rows behind the group's last belong to the next group: their columns of the
+          // accumulator are not stored
 #pragma unroll
           for (int b = C::kBoxes - 1; b >= 0; --b)
             if (half & (16 << b)) {
               const int done = half & ~((32 << b) - 1);
-              tma_load_2d(dst + done * kStageBytes, &xmaps.map[b], k0, row0 + done, bar);
+              tma_load_2d(base + st * C::kStage + done * kStageBytes, &xmaps.map[b], k0, row0 + done, bars + st * 8);
             }
+          if (++st == kStages) st = 0, phase ^= 1;
         }
-        __syncwarp();
-        if (++st == kStages) st = 0, phase ^= 1;
       }
     }
   } else if (warp < 4) {
