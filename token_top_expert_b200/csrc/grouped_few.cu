@@ -187,14 +187,16 @@ int launch(const GroupedArgs& a, const KArgs& k, cudaStream_t st) {
 
 }  // namespace
 
-// Up to 8 rows, unless many weights have short rows, this kernel is the faster one (the matrix
-// unit's time in brackets, cold weights): one token's gate and up, hidden 2048 x 768 channels x
-// 128 experts top-8, 12.1 us (13.9), 8 bits 8.4 (9.6), but its 8-bit down product with k = 768 9.8
-// (6.7); one 4096 x 4096 bf16 weight, 1 row 7.9 us (19), 8 rows 16.4 (19), 12 rows 22.4 (19).
+// Up to 8 rows (4 of one large weight), unless many weights have short rows, this kernel is the
+// faster one (the matrix unit's time in brackets, cold weights): one token's gate and up, hidden
+// 2048 x 768 channels x 128 experts top-8, 12.0 us (13.5), 8 bits 8.4 (9.1), but its 8-bit down
+// product with k = 768 9.8 (6.4); one 4096 x 4096 bf16 weight, 1 row 7.7 us (11.5), 4 rows 10.4
+// (11.6), 8 rows 16.2 (11.7); 1024 x 1024, 8 rows 5.4 (6.4).
 bool few_rows(const GroupedArgs& a) {
   const int64_t kbytes = (int64_t)a.k * (a.i8 ? 1 : 2);
   const int64_t bytes = std::min(a.groups, a.out_rows) * (a.swiglu ? 2 : 1) * kbytes * a.n;
-  return a.w_k == 1 && a.out_rows <= 8 && (kbytes >= 1024 || bytes <= 1 << 20);
+  if (a.w_k != 1 || a.out_rows > (a.groups > 1 || bytes <= 4 << 20 ? 8 : 4)) return false;
+  return kbytes >= 1024 || bytes <= 1 << 20;
 }
 
 int launch_few(const GroupedArgs& a, const KArgs& k, cudaStream_t st) {
