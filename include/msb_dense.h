@@ -37,6 +37,7 @@ extern "C" {
 
 #define MSB_DENSE_MAX_TOKENS 1048576 /* tokens of a route or a dense block */
 #define MSB_GROUPED_MAX_NK 1048576   /* n and k of a grouped product */
+#define MSB_GROUPED_MAX_ROWS 1073741824 /* output rows of a grouped product */
 #define MSB_NORM_MAX_D 16384         /* row length of msb_block_norm */
 #define MSB_INT8_MAX_K 131056        /* inner length of an 8-bit product: the int32 sum of
                                         k products of at most 128^2 stays below 2^31 */
@@ -92,7 +93,7 @@ typedef struct msb_group_weights {
  *           out_rows).  x_rows is at least 1 where out_rows is.  A row outside 0..x_rows-1 reads as zeros.
  *  offsets  int32 [groups + 1] on the device, ascending, within 0..out_rows; NULL with
  *           groups = 1: all rows.  (An offset that is not is moved to the nearest that is.)
- *  out_rows rows of out; 0 is allowed and does nothing.
+ *  out_rows rows of out, up to MSB_GROUPED_MAX_ROWS; 0 is allowed and does nothing.
  *  groups   1..MSB_MAX_EXPERTS; n, k 1..MSB_GROUPED_MAX_NK.
  *  out      out_type (MSB_BF16 or MSB_F32), row p at out + p * ldo elements, ldo >= n; must
  *           not overlap x or the weights.

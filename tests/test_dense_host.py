@@ -78,6 +78,7 @@ def test_grouped_limits_and_empty(lib, st):
     assert matmul(lib, st, groups=513) == st.MSB_EUNSUPPORTED
     assert matmul(lib, st, n=(1 << 20) + 1, ldo=1 << 21) == st.MSB_EUNSUPPORTED
     assert matmul(lib, st, k=(1 << 20) + 1) == st.MSB_EUNSUPPORTED
+    assert matmul(lib, st, out_rows=(1 << 30) + 1, x_rows=(1 << 30) + 1) == st.MSB_EUNSUPPORTED
     assert matmul(lib, st, fn="msb_int8_matmul", k=st.MSB_INT8_MAX_K + 1) == st.MSB_EUNSUPPORTED
     # no rows: nothing to do, nothing launched
     assert matmul(lib, st, out_rows=0, x_rows=0, x=None, out=None) == st.MSB_OK

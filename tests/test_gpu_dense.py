@@ -246,6 +246,35 @@ def test_wide_pitches_and_strided_views(msb):
         assert (ob[:, :3] == 5).all() and (ob[:, 3 + n:] == 5).all()
 
 
+def test_inner_length_of_one(msb):
+    """k = 1: either dimension of the weight may be the contiguous one."""
+    import torch
+    x = rnd(60, 20, 8)[:, :1]
+    for w in (rnd(61, 1, 24, 8)[:, :, :1], rnd(62, 1, 24, 1), rnd(63, 1, 1, 24).transpose(1, 2)):
+        want = x.double() @ w[0].double().t()
+        within(msb.grouped_matmul(x, w), want, (BF16 + F32) * want.abs() + TINY)
+
+
+def test_nothing_to_do(msb):
+    """Calls of no tokens or rows return empty tensors."""
+    import torch
+    w = synth.TINY
+    layer = device_layer(w, rank=0)
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    none = torch.empty((0, w.d), **bf)
+    assert msb.moe_dense_block(none, layer).shape == (0, w.d)
+    assert msb.moe_dense_block(none, msb.Int8Layer.from_packed(layer)).shape == (0, w.d)
+    q, s = msb.quantize_int8(none)
+    assert q.shape == (0, w.d) and s.shape == (0,)
+    assert msb.linear_int8(none, torch.ones(8, w.d, device="cuda", dtype=torch.int8), torch.ones(8, device="cuda")).shape == (0, 8)
+    assert msb.grouped_matmul(none, torch.ones((8, w.d), **bf)).shape == (0, 8)
+    r = msb.route(torch.empty((0, 8), device="cuda"), 2)
+    assert (r.offsets == 0).all()
+    assert msb.combine(none, r).shape == (0, w.d)
+    h, x = msb.block_norm(none, none)
+    assert x.shape == (0, w.d)
+
+
 def test_many_groups(msb):
     """512 groups, most of them empty."""
     import torch

@@ -49,6 +49,7 @@ MSB_BF16 = 0
 MSB_F32 = 1
 MSB_DENSE_MAX_TOKENS = 1048576
 MSB_GROUPED_MAX_NK = 1048576
+MSB_GROUPED_MAX_ROWS = 1 << 30
 MSB_NORM_MAX_D = 16384
 MSB_INT8_MAX_K = 131056
 

@@ -44,7 +44,8 @@ int grouped_check(GroupedArgs& a, const msb_group_weights* w, int32_t out_type) 
   const int64_t es = a.i8 ? 1 : 2;
   if (!w || a.groups < 1 || a.n < 1 || a.k < 1 || a.out_rows < 0 || a.x_rows < 0 || !type_ok(out_type))
     return MSB_EINVAL;
-  if (a.groups > MSB_MAX_EXPERTS || a.n > MSB_GROUPED_MAX_NK || a.k > MSB_GROUPED_MAX_NK || (a.i8 && a.k > MSB_INT8_MAX_K)) return MSB_EUNSUPPORTED;
+  if (a.groups > MSB_MAX_EXPERTS || a.n > MSB_GROUPED_MAX_NK || a.k > MSB_GROUPED_MAX_NK ||
+      a.out_rows > MSB_GROUPED_MAX_ROWS || (a.i8 && a.k > MSB_INT8_MAX_K)) return MSB_EUNSUPPORTED;
   if (!a.offsets && a.groups != 1) return MSB_EINVAL;
   if (!w->data || (a.i8 && !a.w_scale) || (a.out_rows > 0 && (!a.x || !a.out || (a.i8 && !a.x_scale))))
     return MSB_EINVAL;
@@ -56,7 +57,8 @@ int grouped_check(GroupedArgs& a, const msb_group_weights* w, int32_t out_type) 
   a.w = w->data;
   a.w_k = w->stride_k, a.w_n = w->stride_n, a.w_part = w->stride_part, a.w_group = w->stride_group;
   const int parts = a.swiglu ? 2 : 1;
-  const bool m_major = a.w_k != 1;
+  // a single k: n may be the contiguous one
+  const bool m_major = a.w_k != 1 || (a.k == 1 && a.n > 1 && a.w_n == 1 && !a.swiglu && !a.i8);
   if (m_major && (a.w_n != 1 || a.swiglu)) return MSB_EINVAL;
   if (m_major && a.i8) return MSB_EUNSUPPORTED;
   // strides of dimensions of one element say nothing: any that a tensor map takes will do

@@ -22,7 +22,9 @@ int launch_early(void (*kernel)(P...), int64_t blocks, int threads, size_t smem,
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? MSB_OK : MSB_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess) return MSB_OK;
+  cudaGetLastError();  // reported here, not by the next call
+  return MSB_ECUDA;
 }
 
 int route_blocks(int tokens);  // blocks of the routing kernels: rows of their histogram

@@ -9,16 +9,22 @@
 // (a group of c rows is cut into ceil(c / 256) even pieces).  One row streams its experts'
 // weights; a prompt runs at the matrix unit's rate.
 //
-// One CTA pair per tile (persistent, static order), 18 warps a CTA:
+// One CTA pair per tile (persistent, static order), 14 to 18 warps a CTA:
 //   warps 0-3  epilogue: tensor memory -> registers -> scale / SwiGLU -> global
 //   warp 4     issues the matrix instructions (even CTA) into one of two accumulators
 //   warp 5     weights: one, two or eight tensor-map boxes per stage of 128 bytes of k
-//   warps 6-17 rows of x.  In order: boxes of 128, 64, 32 and 16 rows (warp 6).  Gathered: two
-//              warps to a stage copy 16 bytes a thread, asynchronously, into the same swizzle,
-//              wait for them and hand the stage over.  (The fence that makes copied bytes
-//              visible to the matrix unit waits for all copies of its thread, so a stage's
-//              copies are all that its warps have in flight; a gathering tensor-map load, four
-//              rows an instruction, takes the copy unit 60 to 80 cycles for 512 bytes.)
+//   warps 6-   rows of x.  In order: boxes of 128, 64, 32 and 16 rows (warp 6).  Gathered: one or
+//              two warps to a stage copy 16 bytes a thread, asynchronously, into the same
+//              swizzle, wait for them and hand the stage over.  (A gathering tensor-map load,
+//              four rows an instruction, took the copy unit 60 to 80 cycles for 512 bytes: gate
+//              and up of 4096 tokens 497 us, where the rest of the kernel took 254.)
+//
+// What bounds it: weights from memory while the groups are small (64 tokens' gate and up, hidden
+// 2048 x 768 channels x 128 experts top-8, 120 us for 0.79 GB: 6.6 TB/s), then the way from L2 to
+// the SMs, about 80 bytes per nanosecond and SM (a 256 x 256 tile's stage of 64 KB takes its pair
+// 430 ns, the matrix instructions 270 of them): 4096 tokens' gate and up 211 to 240 us, 0.86 to
+// 0.98 PFLOP/s; bf16 8192^3 575 to 600 us, 1.83 to 1.91 PFLOP/s.  Long runs meet the board's
+// power limit and are slower by up to a fifth.
 #include <cuda.h>
 
 #include <algorithm>
@@ -754,14 +760,14 @@ int tile_rows(const GroupedArgs& a, const KArgs& k) {
   if (a.out_f32 && !a.i8) return 64;  // sums in registers
   const int64_t rows = a.out_rows, groups = std::min<int64_t>(a.groups, rows);
   // Few tiles: the smallest that one round of the pairs holds (one 4096 x 4096 bf16 weight, 64-,
-  // 128- and 256-row tiles: 256 rows 19.0, 19.8, 26.4 us; 512 rows 31.9, 20.0, 27.4; 1024 rows
-  // 57, 34, 28).
+  // 128- and 256-row tiles: 256 rows 17.2, 23.1, 32.5 us; 512 rows 28.7, 23.1, 33.6; 1024 rows
+  // 51.7, 33.5, 31.4).
   for (int bn = 64; bn <= 256; bn *= 2)
     if (k.mtiles * std::max(groups, (rows + bn - 1) / bn) <= kPairs) return bn;
   // Many: by the rows of a group, on average (gate and up of hidden 2048 x 768 channels x 128
-  // experts; bf16, 32 rows 131, 129, 137 us; 64 rows 176, 148, 147; 128 rows 256, 199, 167; 8
-  // bits, 16 rows 67, 75, 94; 64 rows 91, 88, 128; 128 rows 137, 120, 125).
-  return rows <= 32 * groups ? 64 : rows <= (a.i8 ? 128 : 64) * groups ? 128 : 256;
+  // experts; bf16, 16 rows 121, 124, 130 us; 64 rows 148, 137, 139; 128 rows 240, 175, 162; 8
+  // bits, 16 rows 67, 75, 80; 64 rows 90, 87, 83; 128 rows 137, 112, 93).
+  return rows <= 32 * groups ? 64 : rows <= 64 * groups ? 128 : 256;
 }
 
 }  // namespace
