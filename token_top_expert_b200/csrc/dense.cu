@@ -222,7 +222,7 @@ int32_t msb_dense_check(void* stream) { return dense_check(static_cast<cudaStrea
 
 size_t msb_route_workspace_size(int32_t tokens, int32_t experts) {
   if (tokens < 0 || tokens > MSB_DENSE_MAX_TOKENS || experts < 1 || experts > MSB_MAX_EXPERTS) return 0;
-  return 4 * (size_t)route_blocks(tokens) * experts;
+  return 4 * (size_t)route_blocks(tokens, experts) * experts;
 }
 
 int32_t msb_route(const void* logits, int32_t logits_type, int64_t ld, const uint8_t* mask,

@@ -27,7 +27,7 @@ int launch_early(void (*kernel)(P...), int64_t blocks, int threads, size_t smem,
   return MSB_ECUDA;
 }
 
-int route_blocks(int tokens);  // blocks of the routing kernels: rows of their histogram
+int route_blocks(int tokens, int experts);  // blocks of the routing kernels: rows of their histogram
 int launch_route(const void* logits, bool bf16, int64_t ld, const uint8_t* mask, int tokens,
                  int experts, int top_e, bool renorm, int32_t* ids, float* weights,
                  int32_t* offsets, int32_t* rows, int32_t* pos, int32_t* hist, cudaStream_t st);
