@@ -152,6 +152,44 @@ def test_one_group_with_few_tiles(msb, R, n, k, gather):
     within(msb.matmul_int8(q, one, w8, ones, rows=rows), want, (BF16 + F32) * want.abs())
 
 
+@pytest.mark.parametrize("counts", [[600, 0, 513, 257, 1300], [2670], [256, 512, 33, 700, 300, 1024, 1, 640]])
+def test_large_groups(msb, counts):
+    """Groups of several pieces and of two accumulators, enough of them for the largest tiles: each
+    kind of product, in order and gathered.  Tolerances as above."""
+    import torch
+    k, T, E, R = 136, 900, len(counts), sum(counts)
+    offs = offsets_of(counts)
+    rows = torch.randint(-1, T + 1, (R,), device="cuda", dtype=torch.int32)
+    xs, xg = rnd(70, R, k), rnd(71, T, k)
+    for x, idx in ((xs, None), (xg, rows)):
+        for layout in ("k", "records"):
+            n = 4104
+            w = weight(72, E, n, k, layout)
+            want, mag = product64(x, w, offs, idx)
+            within(msb.grouped_matmul(x, w, offs, rows=idx), want, BF16 * want.abs() + k * 2 * F32 * mag + TINY, layout)
+        n = 2072
+        w = weight(73, 2 * E, n, k, "k").unflatten(0, (E, 2))
+        (g, ga), (u, ua) = (product64(x, w[:, p], offs, idx) for p in range(2))
+        dg, du, sg = k * 2 * F32 * ga, k * 2 * F32 * ua, torch.nn.functional.silu(g)
+        tol = (BF16 + 2.0 ** -20) * (sg * u).abs() + 1.1 * dg * u.abs() + sg.abs() * du + 1.1 * dg * du + TINY
+        within(msb.grouped_swiglu(x, w, offs, rows=idx), sg * u, tol + 2.0 ** -117 * u.abs(), "swiglu")
+        n = 4104
+        q, qs = msb.quantize_int8(x)
+        w8 = torch.randint(-127, 128, (E, n, 144), device="cuda").to(torch.int8)[..., :k]
+        ws = rnd(74, E, n, dtype=torch.float32)
+        want = product64(q, w8, offs, idx)[0]
+        if idx is None:
+            want = want * qs.double()[:, None]
+        else:
+            ok = (idx >= 0) & (idx < T)
+            want = want * torch.where(ok, qs[idx.long().clamp(0, T - 1)], 0.0).double()[:, None]
+        for e, (lo, hi) in enumerate(zip(offs.tolist(), offs.tolist()[1:])):
+            want[lo:hi] *= ws[e].double()
+        for dtype, step in ((torch.bfloat16, BF16), (torch.float32, 0)):
+            got = msb.matmul_int8(q, qs, w8, ws, offs, rows=idx, out_dtype=dtype)
+            within(got, want, (step + 3.1 * F32) * want.abs() + TINY, ("int8", dtype))
+
+
 def test_float_outputs_keep_float_precision(msb):
     """Float outputs at k = 8192: the sum is cut off every 256 k only, each time by less than 2^-23
     of a part's size per addition; relative L2 below 1e-6 (the bf16 output's rounding is 2e-3)."""

@@ -765,8 +765,8 @@ int tile_rows(const GroupedArgs& a, const KArgs& k) {
   for (int bn = 64; bn <= 256; bn *= 2)
     if (k.mtiles * std::max(groups, (rows + bn - 1) / bn) <= kPairs) return bn;
   // Many: by the rows of a group, on average (gate and up of hidden 2048 x 768 channels x 128
-  // experts; bf16, 16 rows 121, 124, 130 us; 64 rows 148, 137, 139; 128 rows 240, 175, 162; 8
-  // bits, 16 rows 67, 75, 80; 64 rows 90, 87, 83; 128 rows 137, 112, 93).
+  // experts; bf16, 16 rows 120, 122, 128 us; 64 rows 148, 135, 138; 128 rows 240, 175, 157; 8
+  // bits, 16 rows 66, 67, 72; 64 rows 82, 75, 77; 128 rows 121, 92, 83).
   return rows <= 32 * groups ? 64 : rows <= 64 * groups ? 128 : 256;
 }
 
