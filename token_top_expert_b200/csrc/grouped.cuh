@@ -28,14 +28,25 @@ struct KArgs {
 // [0, out_rows] or below an earlier one are raised or cut to it, so that no offsets lead
 // outside the buffers.
 __device__ inline void group_begins(const KArgs& a, int32_t* begin, int lane) {
+  // eight loads in flight: one memory latency for up to 255 groups
+  for (int b = 0; b <= a.groups; b += 256) {
+    int o[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int e = b + q * 32 + lane;
+      o[q] = e > a.groups ? 0 : a.offsets ? a.offsets[e] : e ? a.out_rows : 0;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int e = b + q * 32 + lane;
+      if (e <= a.groups) begin[e] = min(max(o[q], 0), a.out_rows);
+    }
+  }
+  __syncwarp();
   const int per = (a.groups + 32) >> 5;  // of groups + 1 offsets
   const int e0 = lane * per, e1 = min(e0 + per, a.groups + 1);
   int top = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int o = a.offsets ? a.offsets[e] : e ? a.out_rows : 0;
-    top = max(top, min(o, a.out_rows));
-    begin[e] = top;
-  }
+  for (int e = e0; e < e1; ++e) begin[e] = top = max(top, begin[e]);
   int above = top;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {

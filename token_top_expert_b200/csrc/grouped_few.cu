@@ -35,10 +35,6 @@ __device__ void find_used(const KArgs& a, Used& s) {
   __syncthreads();
 }
 
-__device__ __forceinline__ const uint8_t* x_row(const KArgs& a, int p) {
-  const int row = a.rows ? a.rows[p] : p;
-  return (uint32_t)row < (uint32_t)a.x_rows ? a.x + (int64_t)row * a.pitch : nullptr;
-}
 __device__ __forceinline__ float x_scale(const KArgs& a, int p) {
   const int row = a.rows ? a.rows[p] : p;
   return (uint32_t)row < (uint32_t)a.x_rows ? a.x_scale[row] : 0.f;
@@ -69,15 +65,22 @@ __device__ __forceinline__ uint4 load_part(const uint8_t* p, int valid) {
 
 constexpr int kResident = 2;  // blocks of an SM
 
-// P pieces of two weight rows, 32 pieces apart, times R rows of x.
+// P pieces of two weight rows, 32 pieces apart, times R rows of x.  The rows' indices may still be
+// on their way: they are not looked at before the weights' loads are under way.
 template <int P, int R, class Acc>
-__device__ __forceinline__ void few_pieces(const uint8_t* w0, const uint8_t* w1, const uint8_t* const (&x)[R],
+__device__ __forceinline__ void few_pieces(const KArgs& a, const uint8_t* w0, const uint8_t* w1, int (&row)[R],
                                            int64_t at, Acc (&acc)[2][R]) {
   uint4 v[2][P];
 #pragma unroll
   for (int q = 0; q < P; ++q) v[0][q] = load_stream(w0 + at + q * 512);
 #pragma unroll
   for (int q = 0; q < P; ++q) v[1][q] = load_stream(w1 + at + q * 512);
+  const uint8_t* x[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    asm volatile("" : "+r"(row[r]));
+    x[r] = a.x + (int64_t)((uint32_t)row[r] < (uint32_t)a.x_rows ? row[r] : 0) * a.pitch;
+  }
 #pragma unroll
   for (int q = 0; q < P; ++q)
 #pragma unroll
@@ -96,27 +99,23 @@ __device__ __forceinline__ void few_rows_of(const KArgs& a, const uint8_t* w0, c
   using Acc = typename std::conditional<I8, int, float>::type;
   constexpr int P = R == 4 ? 4 : 8;
   const int whole = a.kbytes >> 4, tail = a.kbytes & 15;
-  const uint8_t* x[R];
-  uint32_t there = 0;  // rows that are inside x: the others give zeros (and read the first row)
+  int row[R];  // of x; one outside gives zeros (and reads the first)
   Acc acc[2][R] = {};
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const uint8_t* const row = x_row(a, p0 + r);
-    there |= (uint32_t)(row != nullptr) << r;
-    x[r] = row ? row : a.x;
-  }
+  for (int r = 0; r < R; ++r) row[r] = a.rows ? a.rows[p0 + r] : p0 + r;
   int i = lane;
-  for (; i + 32 * (P - 1) < whole; i += 32 * P) few_pieces<P>(w0, w1, x, (int64_t)i * 16, acc);
+  for (; i + 32 * (P - 1) < whole; i += 32 * P) few_pieces<P>(a, w0, w1, row, (int64_t)i * 16, acc);
   if (P == 8 && i + 96 < whole) {
-    few_pieces<4>(w0, w1, x, (int64_t)i * 16, acc);
+    few_pieces<4>(a, w0, w1, row, (int64_t)i * 16, acc);
     i += 128;
   }
-  for (; i < whole; i += 32) few_pieces<1>(w0, w1, x, (int64_t)i * 16, acc);
+  for (; i < whole; i += 32) few_pieces<1>(a, w0, w1, row, (int64_t)i * 16, acc);
   if (tail && lane == 0) {
     const uint4 v0 = load_part(w0 + (int64_t)whole * 16, tail), v1 = load_part(w1 + (int64_t)whole * 16, tail);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const uint4 xv = load_part(x[r] + (int64_t)whole * 16, tail);
+      const int64_t at = (uint32_t)row[r] < (uint32_t)a.x_rows ? row[r] : 0;
+      const uint4 xv = load_part(a.x + at * a.pitch + (int64_t)whole * 16, tail);
       dot16(v0, xv, acc[0][r]);
       dot16(v1, xv, acc[1][r]);
     }
@@ -128,7 +127,7 @@ __device__ __forceinline__ void few_rows_of(const KArgs& a, const uint8_t* w0, c
       acc[0][r] += __shfl_xor_sync(0xffffffffu, acc[0][r], o);
       acc[1][r] += __shfl_xor_sync(0xffffffffu, acc[1][r], o);
     }
-    if (!(there >> r & 1)) acc[0][r] = acc[1][r] = 0;
+    if ((uint32_t)row[r] >= (uint32_t)a.x_rows) acc[0][r] = acc[1][r] = 0;
   }
   const int c = ch + (GATED ? 0 : lane);
   if (lane >= (GATED ? 1 : 2) || c >= a.n) return;
