@@ -550,6 +550,14 @@ def test_block_norm(msb, R, d, h32, y32, gate):
     assert ho2 is h and torch.equal(h, ho) and torch.equal(x2, x)
 
 
+@pytest.mark.parametrize("R,d", [(1183, 2048), (1184, 1032), (2500, 1536), (1500, 768), (1300, 264)])
+@pytest.mark.parametrize("h32,y32", [(True, False), (False, False), (True, True), (False, True)])
+def test_block_norm_many_rows(msb, R, d, h32, y32):
+    """Row counts on both sides of the choice of threads, blocks that take several rows."""
+    for gate in ("token", "full"):
+        test_block_norm(msb, R, d, h32, y32, gate)
+
+
 def test_block_norm_is_residual_rmsnorm(msb):
     """Without weights, gate and scales it is the decode stack's glue."""
     import torch

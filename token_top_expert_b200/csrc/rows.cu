@@ -81,6 +81,27 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
 
 __host__ __device__ constexpr int block_threads(int nt) { return nt == 32 ? 256 : nt; }
 
+// Two neighbouring elements.  PAIR: one instruction works on both.
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+template <bool PAIR>
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  if constexpr (!PAIR) return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+  float2 r;
+  asm("{.reg .b64 a, b, c, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 r, a, b, c;\n mov.b64 {%0, %1}, r;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+template <bool PAIR>
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  if constexpr (!PAIR) return make_float2(a.x * b.x, a.y * b.y);
+  float2 r;
+  asm("{.reg .b64 a, b, r;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      "mul.rn.f32x2 r, a, b;\n mov.b64 {%0, %1}, r;}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 // Eight elements as they lie in memory.
 template <bool F32>
 struct Raw {
@@ -100,7 +121,25 @@ struct Raw {
       v[4] = bf16_lo(a[0].z), v[5] = bf16_hi(a[0].z), v[6] = bf16_lo(a[0].w), v[7] = bf16_hi(a[0].w);
     }
   }
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
+    float f[8];
+    get(f);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = make_float2(f[2 * c], f[2 * c + 1]);
+  }
 };
+__device__ __forceinline__ void load_two(const void* p, bool f32, int64_t i, float2 (&v)[4]) {
+  float f[8];
+  load_w<8>(p, f32, i, f);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v[c] = make_float2(f[2 * c], f[2 * c + 1]);
+}
+__device__ __forceinline__ void store_two(void* p, bool f32, int64_t i, const float2 (&v)[4]) {
+  float f[8];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) f[2 * c] = v[c].x, f[2 * c + 1] = v[c].y;
+  store_w<8>(p, f32, i, f);
+}
 
 // ------------------------------------------------------------------ 8-bit quantisation
 
@@ -274,45 +313,20 @@ __global__ void __launch_bounds__(kCombineNT)
 
 // ------------------------------------------------------------------ block norm
 
-// The branch's elements of a row: [rms](y) * post * gate.
-template <int W>
-__device__ __forceinline__ void branch(const NormArgs& a, int64_t t, int i, float yscale, float (&b)[W]) {
-  float m[W];
-#pragma unroll
-  for (int c = 0; c < W; ++c) b[c] *= yscale;
-  if (a.post) {
-    load_w<W>(a.post, a.w_f32, i, m);
-#pragma unroll
-    for (int c = 0; c < W; ++c) b[c] *= m[c];
-  }
-  if (!a.gate) return;
-  if (a.gate_col == 0) {
-    const float g = load(a.gate, a.gate_f32, t * a.gate_row);
-#pragma unroll
-    for (int c = 0; c < W; ++c) m[c] = g;
-  } else if (W > 1 && a.gate_col == 1) {
-    load_w<W>(a.gate, a.gate_f32, t * a.gate_row + i, m);
-  } else {
-#pragma unroll
-    for (int c = 0; c < W; ++c) m[c] = load(a.gate, a.gate_f32, t * a.gate_row + (i + c) * a.gate_col);
-  }
-#pragma unroll
-  for (int c = 0; c < W; ++c) b[c] *= m[c];
-}
-
 // Blocks of an SM that the registers are cut to: more keep more loads in flight, fewer do not
-// spill (8192 x 4096, 4 and 3 blocks: bf16 48.5 and 51.4 us, float h 75.7 and 64.8; 8192 x 2048,
-// 6 and 4 blocks: 37.1 and 29.2).
+// spill (8192 x 4096, 4 and 3 blocks: bf16 48.5 and 51.4 us, float h 75.7 and 64.8).
 template <int NT, int V, bool F32>
 constexpr int kNormBlocks = (V == 4 ? 2 : V == 2 && F32 ? 3 : 4) * 256 / block_threads(NT);
 
 // b = [rms](y), h' = skip h + residual gate b, x = rms(h'), rows in 16-byte pieces.  The blocks
 // stay and take row after row: while a row's two sums cross the block, the next row's pieces
-// are on their way.  8192 x 4096 bf16: 48.5 us, 5.5 TB/s (77 us with a block per row), where the
-// issue slots are three quarters full.
+// are on their way.  bf16 rows are bound by the instructions (two thirds of the issue slots), so
+// these work on two elements at a time (8192 x 4096: 46.8 us, 5.7 TB/s; 48.5 one by one, 77 with
+// a block per row); float rows need the registers more (64.6 us, 6.2 TB/s; 66.8 in pairs).
 template <int NT, int V, bool HF32, bool YF32>
 __global__ void __launch_bounds__(block_threads(NT), kNormBlocks<NT, V, HF32 || YF32>) block_norm_kernel(const NormArgs a) {
   constexpr int kRows = block_threads(NT) / NT;
+  constexpr bool PAIR = !HF32 && !YF32;
   alignas(16) __shared__ float red[2][2][NT / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -340,51 +354,74 @@ __global__ void __launch_bounds__(block_threads(NT), kNormBlocks<NT, V, HF32 || 
     fetch(t + step);
     float yscale = 1.f;
     if (a.post_norm) {
-      float ss = 0.f;
+      float2 ss = two(0.f);
 #pragma unroll
       for (int j = 0; j < V; ++j)
         if ((j * NT + tid) * 8 < a.d) {
-          float y[8];
+          float2 y[4];
           yr[j].get(y);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) ss = fmaf(y[c], y[c], ss);
+          for (int c = 0; c < 4; ++c) ss = fma2<PAIR>(y[c], y[c], ss);
         }
-      yscale = rsqrtf(fmaf(row_sum<NT>(ss, red[turn][0]), a.inv_d, a.eps));
+      yscale = rsqrtf(fmaf(row_sum<NT>(ss.x + ss.y, red[turn][0]), a.inv_d, a.eps));
     }
-    float h[V][8], ss = 0.f;
+    float2 h[V][4], ss = two(0.f);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int i = (j * NT + tid) * 8;
       if (i >= a.d) continue;
       hr[j].get(h[j]);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) h[j][c] *= a.skip;
+      for (int c = 0; c < 4; ++c) h[j][c] = mul2<PAIR>(h[j][c], two(a.skip));
       if (a.y) {
-        float b[8];
+        float2 b[4], m[4];
         yr[j].get(b);
-        branch<8>(a, t, i, yscale, b);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) h[j][c] = fmaf(a.residual, b[c], h[j][c]);
+        for (int c = 0; c < 4; ++c) b[c] = mul2<PAIR>(b[c], two(yscale));
+        if (a.post) {
+          load_two(a.post, a.w_f32, i, m);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) b[c] = mul2<PAIR>(b[c], m[c]);
+        }
+        if (a.gate) {
+          if (a.gate_col == 0) {
+            const float g = load(a.gate, a.gate_f32, t * a.gate_row);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) m[c] = two(g);
+          } else if (a.gate_col == 1) {
+            load_two(a.gate, a.gate_f32, t * a.gate_row + i, m);
+          } else {
+            float g[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) g[c] = load(a.gate, a.gate_f32, t * a.gate_row + (i + c) * a.gate_col);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) m[c] = make_float2(g[2 * c], g[2 * c + 1]);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) b[c] = mul2<PAIR>(b[c], m[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) h[j][c] = fma2<PAIR>(two(a.residual), b[c], h[j][c]);
       }
 #pragma unroll
-      for (int c = 0; c < 8; ++c) ss = fmaf(h[j][c], h[j][c], ss);
-      if (a.h_out) store_w<8>(a.h_out, HF32, t * a.ldh_out + i, h[j]);
+      for (int c = 0; c < 4; ++c) ss = fma2<PAIR>(h[j][c], h[j][c], ss);
+      if (a.h_out) store_two(a.h_out, HF32, t * a.ldh_out + i, h[j]);
     }
     if (!a.x) continue;
-    const float inv = rsqrtf(fmaf(row_sum<NT>(ss, red[turn][1]), a.inv_d, a.eps));
+    const float inv = rsqrtf(fmaf(row_sum<NT>(ss.x + ss.y, red[turn][1]), a.inv_d, a.eps));
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int i = (j * NT + tid) * 8;
       if (i >= a.d) continue;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) h[j][c] *= inv;
+      for (int c = 0; c < 4; ++c) h[j][c] = mul2<PAIR>(h[j][c], two(inv));
       if (a.pre) {
-        float m[8];
-        load_w<8>(a.pre, a.w_f32, i, m);
+        float2 m[4];
+        load_two(a.pre, a.w_f32, i, m);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) h[j][c] *= m[c];
+        for (int c = 0; c < 4; ++c) h[j][c] = mul2<PAIR>(h[j][c], m[c]);
       }
-      store_w<8>(a.x, false, t * a.ldx + i, h[j]);
+      store_two(a.x, false, t * a.ldx + i, h[j]);
     }
   }
 }
@@ -512,23 +549,21 @@ int norm_rows(const NormArgs& a, cudaStream_t st) {
   }
 }
 
-// f(NT, W, V) for the smallest shape that holds k elements a row.
-#define MSB_ROW_SHAPES(wide, k, F)                        \
-  if (wide) {                                             \
-    if ((k) <= 256) return F(32, 8, 1);                   \
-    if ((k) <= 512) return F(32, 8, 2);                   \
-    if ((k) <= 1024) return F(32, 8, 4);                  \
-    if ((k) <= 2048) return F(256, 8, 1);                 \
-    if ((k) <= 4096) return F(256, 8, 2);                 \
-    if ((k) <= 8192) return F(512, 8, 2);                 \
-    if ((k) <= 16384) return F(512, 8, 4);                \
-  } else {                                                \
-    if ((k) <= 128) return F(32, 1, 4);                   \
-    if ((k) <= 512) return F(32, 1, 16);                  \
-    if ((k) <= 1024) return F(256, 1, 4);                 \
-    if ((k) <= 4096) return F(256, 1, 16);                \
-    if ((k) <= 16384) return F(512, 1, 32);               \
-  }
+// F(NT, W, V) for the smallest shape that holds k elements a row: in eights, one by one.
+#define MSB_ROW_SHAPES_8(k, F)                  \
+  if ((k) <= 256) return F(32, 8, 1);           \
+  if ((k) <= 512) return F(32, 8, 2);           \
+  if ((k) <= 1024) return F(32, 8, 4);          \
+  if ((k) <= 2048) return F(256, 8, 1);         \
+  if ((k) <= 4096) return F(256, 8, 2);         \
+  if ((k) <= 8192) return F(512, 8, 2);         \
+  if ((k) <= 16384) return F(512, 8, 4);
+#define MSB_ROW_SHAPES_1(k, F)                  \
+  if ((k) <= 128) return F(32, 1, 4);           \
+  if ((k) <= 512) return F(32, 1, 16);          \
+  if ((k) <= 1024) return F(256, 1, 4);         \
+  if ((k) <= 4096) return F(256, 1, 16);        \
+  if ((k) <= 16384) return F(512, 1, 32);
 
 }  // namespace
 
@@ -544,7 +579,11 @@ int launch_quantize(const void* x, bool f32, int64_t ldx, int rows, int k, int8_
 #define MSB_QUANT(NT, W, V)                                                                          \
   launch_early(quantize_kernel<NT, W, V>, ((int64_t)rows * NT + block_threads(NT) - 1) / block_threads(NT), \
          block_threads(NT), 0, st, x, f32, ldx, rows, k, q, ldq, scale)
-  MSB_ROW_SHAPES(wide, k, MSB_QUANT)
+  if (wide) {
+    MSB_ROW_SHAPES_8(k, MSB_QUANT)
+  } else {
+    MSB_ROW_SHAPES_1(k, MSB_QUANT)
+  }
 #undef MSB_QUANT
   return launch_early(quantize_long_kernel, rows, 256, 0, st, x, f32, ldx, k, q, ldq, scale);
 }
@@ -569,8 +608,21 @@ int launch_block_norm(const NormArgs& a, cudaStream_t st) {
               by8(a.h_out, a.h_out ? a.ldh_out : 0, rows) && by8(a.x, a.x ? a.ldx : 0, rows) &&
               by8(a.pre, 0, 1) && by8(a.post, 0, 1);
   if (a.gate && a.gate_col == 1) wide = wide && by8(a.gate, a.gate_row, rows);
+  const bool f32 = a.h_f32 || a.y_f32;
 #define MSB_NORM(NT, W, V) norm_rows<NT, W, V>(a, st)
-  MSB_ROW_SHAPES(wide, a.d, MSB_NORM)
+  if (!wide) {
+    MSB_ROW_SHAPES_1(a.d, MSB_NORM)
+  }
+  // Rows in eights: threads and pieces a thread that keep the loads of about 64 KB in flight on
+  // an SM where there are rows for it (8192 x 2048, 128 and 256 threads: bf16 24.9 and 29.6 us; 4
+  // x 2048 2.6 and 2.1; float h, 8192 x 1024, 128 threads and a warp: 18.5 and 23.7).
+  if (a.d <= 256) return MSB_NORM(32, 8, 1);
+  if (a.d <= 512) return MSB_NORM(32, 8, 2);
+  if (a.d <= 1024) return f32 ? MSB_NORM(128, 8, 1) : MSB_NORM(32, 8, 4);
+  if (a.d <= 2048) return rows >= kManyRows ? MSB_NORM(128, 8, 2) : MSB_NORM(256, 8, 1);
+  if (a.d <= 4096) return MSB_NORM(256, 8, 2);
+  if (a.d <= 8192) return MSB_NORM(512, 8, 2);
+  if (a.d <= 16384) return MSB_NORM(512, 8, 4);
 #undef MSB_NORM
   return MSB_EUNSUPPORTED;  // d <= MSB_NORM_MAX_D
 }
