@@ -497,20 +497,20 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(Cfg<BN>::kTh
     const uint32_t base = smem_addr(stages) + st * C::kStage + kABytes + r0 * kStageBytes;
     uint32_t phase = 0;
     int at = 0;  // stages before this tile, modulo the ring
-    int next[C::kLaneRows], half = 0, nhalf = 0;  // row indices are fetched a tile ahead
+    int next[C::kLaneRows], nmine = 0, nrows = 0;  // row indices are fetched a tile ahead
     const auto fetch = [&](int t) {
       if (t >= tiles) return;
       const Tile tile = tile_at(a, s, t);
-      nhalf = ((tile.rows + 31) & ~31) >> 1;  // this CTA's rows of the tile
-      const int p0 = (int)rank * nhalf + part * (nhalf / kSplit) + r0;
+      nmine = ((tile.rows + 31) & ~31) / (2 * kSplit);  // this warp's: 8, 16, .. C::kLaneRows * 4
+      const int p0 = ((int)rank * kSplit + part) * nmine + r0;
+      // and this lane's, four apart; what lies behind the tile's last row is not stored, nor copied
+      nrows = min(nmine, tile.rows - p0);
 #pragma unroll
-      for (int q = 0; q < C::kLaneRows; ++q)
-        next[q] = q * 4 < nhalf / kSplit && p0 + q * 4 < tile.rows ? a.rows[tile.row0 + p0 + q * 4] : -1;
+      for (int q = 0; q < C::kLaneRows; ++q) next[q] = q * 4 < nrows ? a.rows[tile.row0 + p0 + q * 4] : 0;
     };
     fetch(pair);
     for (int t = pair; ok && t < tiles; t += pairs) {
-      half = nhalf;
-      const int mine = half / kSplit;  // this warp's: 8, 16, .. C::kLaneRows * 4 from part * mine on
+      const int mine = nmine, rows = nrows;
       const uint8_t* src[C::kLaneRows];
       uint32_t there = 0;  // rows that exist
 #pragma unroll
@@ -519,6 +519,8 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(Cfg<BN>::kTh
         there |= (uint32_t)use << q;
         src[q] = a.x + (use ? (int64_t)next[q] * a.pitch + chunk * 16 : 0);
       }
+      const bool all = __all_sync(0xffffffffu, there == ~0u >> (32 - C::kLaneRows));
+      const uint32_t dst = base + part * mine * kStageBytes;
       fetch(t + pairs);
       int i = st - at;
       if (i < 0) i += kStages;
@@ -528,12 +530,19 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(Cfg<BN>::kTh
         phase ^= 1;
         const int left = a.kbytes - (kb + i) * kStageBytes - chunk * 16;
         const uint32_t valid = left < 0 ? 0 : left > 16 ? 16 : left;
-        const int64_t k0 = valid ? (int64_t)(kb + i) * kStageBytes : 0;
+        const uint32_t k0 = valid ? (kb + i) * kStageBytes : 0;
+        const uint32_t even = dst + ((chunk ^ r0) << 4), odd = dst + ((chunk ^ (4 + r0)) << 4);
+        if (all) {
 #pragma unroll
-        for (int q = 0; q < C::kLaneRows; ++q)
-          if (q * 4 < mine)
-            cp_async16(base + (part * mine + q * 4) * kStageBytes + ((chunk ^ ((q * 4 + r0) & 7)) << 4),
-                       src[q] + (there >> q & 1 ? k0 : 0), there >> q & 1 ? valid : 0);
+          for (int q = 0; q < C::kLaneRows; ++q)
+            if (q * 4 < rows) cp_async16((q & 1 ? odd : even) + q * 4 * kStageBytes, src[q] + k0, valid);
+        } else {  // zeros for rows outside x
+#pragma unroll
+          for (int q = 0; q < C::kLaneRows; ++q)
+            if (q * 4 < rows)
+              cp_async16((q & 1 ? odd : even) + q * 4 * kStageBytes, src[q] + (there >> q & 1 ? k0 : 0),
+                         there >> q & 1 ? valid : 0);
+        }
         cp_async_wait_all();
         fence_proxy_async();
         __syncwarp();
