@@ -428,6 +428,37 @@ def test_swiglu_int8(msb, n, k):
     assert torch.equal(got, msb.matmul_int8(q, qs, w, ws, offs, rows=rows, swiglu=True))
 
 
+@pytest.mark.parametrize("R", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("k", [16, 33, 1023, 1032, 2048, 4096])
+@pytest.mark.parametrize("f32,lead,pitch", [(False, 0, 0), (True, 0, 8), (False, 1, 8), (True, 3, 5)])
+def test_linear_int8_is_quantize_and_matmul(msb, R, k, f32, lead, pitch):
+    """The same bits, whichever kernel rounds x; strided and unaligned rows in a buffer of NaN, a
+    row of zeros, one with a NaN."""
+    import torch
+    dtype = torch.float32 if f32 else torch.bfloat16
+    buf = torch.full((lead + R * (k + pitch),), float("nan"), device="cuda", dtype=dtype)
+    x = buf[lead:].view(R, k + pitch)[:, :k]
+    x.copy_(rnd(27, R, k, dtype=dtype))
+    if R > 3:
+        x[2] = 0
+        x[3, k // 2] = float("nan")
+    n, E = 37, 5
+    q, qs = msb.quantize_int8(x)
+    w = torch.randint(-128, 128, (E, 2, n, (k + 15) // 16 * 16), device="cuda").to(torch.int8)[..., :k]
+    ws = rnd(28, E, 2, n, dtype=torch.float32).abs() * 1e-3
+    same = lambda a, b: torch.equal(a, b) or torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())  # noqa: E731
+    for o in (torch.bfloat16, torch.float32):
+        assert same(msb.linear_int8(x, w[1, 0], ws[1, 0], out_dtype=o), msb.matmul_int8(q, qs, w[1, 0], ws[1, 0], out_dtype=o))
+    # grouped: a group of none, rows taken twice, one outside x
+    rows = torch.arange(6, device="cuda", dtype=torch.int32) % R
+    rows[4] = R
+    offs = torch.tensor([0, 1, 1, 4, 5, 6], device="cuda", dtype=torch.int32)
+    assert same(msb.linear_int8(x, w[:, 0], ws[:, 0].contiguous(), offs, rows=rows),
+                msb.matmul_int8(q, qs, w[:, 0], ws[:, 0].contiguous(), offs, rows=rows))
+    assert same(msb.swiglu_int8(x, w, ws, offs, rows=rows),
+                msb.matmul_int8(q, qs, w, ws, offs, rows=rows, swiglu=True))
+
+
 # ------------------------------------------------------------------ routing
 
 def route_ref(l, top_e, renorm, mask):

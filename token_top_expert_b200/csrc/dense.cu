@@ -183,19 +183,17 @@ int dense_block(const void* x, int32_t tokens, const uint8_t* mask, const void* 
   if (w.int8) {
     int8_t* const q = reinterpret_cast<int8_t*>(ws + L.q);
     int8_t* const hq = reinterpret_cast<int8_t*>(ws + L.hq);
-    rc = launch_quantize(x, false, d, tokens, m.d, q, d, f32(L.q_scale), st);
-    if (rc != MSB_OK) return rc;
     g = {w.gate_up, 2 * I * d, I * d, d, 1};
     a = grouped_args(q, d, tokens, i32(L.rows), i32(L.offsets), m.experts, r, m.inter, m.d, ws + L.h, ipad);
     a.i8 = a.swiglu = true, a.x_scale = f32(L.q_scale), a.w_scale = w.gate_up_scale;
-    rc = grouped(a, &g, MSB_BF16, st);
-    if (rc != MSB_OK) return rc;
-    rc = launch_quantize(ws + L.h, false, ipad, r, m.inter, hq, ipad, f32(L.h_scale), st);
+    rc = grouped_check(a, &g, MSB_BF16);
+    if (rc == MSB_OK) rc = launch_linear(a, x, false, d, q, f32(L.q_scale), st);
     if (rc != MSB_OK) return rc;
     g = {w.down, d * ipad, 0, ipad, 1};
     a = grouped_args(hq, ipad, r, nullptr, i32(L.offsets), m.experts, r, m.d, m.inter, ws + L.y, d);
     a.i8 = true, a.x_scale = f32(L.h_scale), a.w_scale = w.down_scale;
-    rc = grouped(a, &g, MSB_BF16, st);
+    rc = grouped_check(a, &g, MSB_BF16);
+    if (rc == MSB_OK) rc = launch_linear(a, ws + L.h, false, ipad, hq, f32(L.h_scale), st);
   } else {
     g = {w.gate_up, 3 * d * I, d, 3 * d, 1};
     a = grouped_args(x, d, tokens, i32(L.rows), i32(L.offsets), m.experts, r, m.inter, m.d, ws + L.h, ipad);
@@ -319,10 +317,9 @@ int32_t msb_int8_linear(const void* x, int32_t x_type, int64_t ldx, int32_t x_ro
   GroupedArgs a = grouped_args(q, pitch, x_rows, rows, offsets, groups, out_rows, n, k, out, ldo);
   a.i8 = true, a.swiglu = swiglu != 0, a.x_scale = scale, a.w_scale = w_scale;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int rc = grouped_check(a, w, out_type);
+  const int rc = grouped_check(a, w, out_type);
   if (rc != MSB_OK || out_rows == 0) return rc;
-  if (x_rows > 0) rc = launch_quantize(x, x_type == MSB_F32, ldx, x_rows, k, q, pitch, scale, st);
-  return rc != MSB_OK ? rc : launch_grouped(a, st);
+  return launch_linear(a, x, x_type == MSB_F32, ldx, q, scale, st);
 }
 
 int32_t msb_combine(const void* y, int32_t y_type, int64_t ldy, int32_t y_rows, const int32_t* pos,

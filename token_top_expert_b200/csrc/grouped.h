@@ -26,6 +26,11 @@ struct GroupedArgs {
 
 int launch_grouped(const GroupedArgs& a, cudaStream_t st);
 
+// x (bf16 or float, rows ldx elements apart) to 8 bits, then the product: a.x = q and a.x_scale =
+// scale are scratch for it, unless one kernel does both.
+int launch_linear(const GroupedArgs& a, const void* x, bool f32, int64_t ldx, int8_t* q, float* scale,
+                  cudaStream_t st);
+
 // Reads and clears the sticky error word of the current device (synchronises the stream).
 int dense_check(cudaStream_t st);
 

@@ -8,6 +8,7 @@
 
 #include "dense.h"
 #include "grouped.cuh"
+#include "quant.cuh"
 
 namespace msb {
 namespace {
@@ -150,12 +151,8 @@ __device__ __forceinline__ void few_rows_of(const KArgs& a, const uint8_t* w0, c
 
 // A warp takes two weight rows (gate and up of a channel, or two channels) at a time.
 template <bool I8, bool GATED, bool F32>
-__global__ void __launch_bounds__(256, kResident) few_kernel(const KArgs a) {
-  __shared__ Used s;
+__device__ __forceinline__ void few_items(const KArgs& a, const Used& s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  find_used(a, s);
   const int each = GATED ? a.n : (a.n + 1) / 2;  // pairs of weight rows of a group
   const int64_t items = (int64_t)s.count * each;
   for (int64_t item = (int64_t)blockIdx.x * 8 + warp; item < items; item += (int64_t)gridDim.x * 8) {
@@ -174,14 +171,119 @@ __global__ void __launch_bounds__(256, kResident) few_kernel(const KArgs a) {
 }
 
 template <bool I8, bool GATED, bool F32>
-int launch(const GroupedArgs& a, const KArgs& k, cudaStream_t st) {
+__global__ void __launch_bounds__(256, kResident) few_kernel(const KArgs a) {
+  __shared__ Used s;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  find_used(a, s);
+  few_items<I8, GATED, F32>(a, s);
+}
+
+// Rows of x before they are quantised.  by8: eights of elements are 16-byte aligned.
+struct RawRows {
+  const void* x;
+  int64_t ldx;
+  bool f32, by8;
+};
+
+// Elements i .. i + 7 of a row, zeros behind its end.
+__device__ __forceinline__ void raw8(const RawRows& r, int64_t row, int i, int k, float (&v)[8]) {
+  const int64_t at = row * r.ldx + i;
+  if (r.by8 && i + 8 <= k) {
+    if (r.f32) {
+      const float4 lo = reinterpret_cast<const float4*>(static_cast<const float*>(r.x) + at)[0];
+      const float4 hi = reinterpret_cast<const float4*>(static_cast<const float*>(r.x) + at)[1];
+      v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(r.x) + at);
+      v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
+      v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
+    }
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    v[c] = i + c >= k ? 0.f
+           : r.f32    ? static_cast<const float*>(r.x)[at + c]
+                      : bf16_lo(static_cast<const uint16_t*>(r.x)[at + c]);
+}
+
+// Rows of x that one launch quantises on the way, and elements with them in sixteens.  One launch
+// and two, cold weights: 1 x 4096, 4096 channels 6.6 and 6.6 us (a call of 14.5 us on the host
+// against 16.1), 1 x 1024, 1024 channels 3.5 and 4.3, 8 x 512, 2048 channels 5.5 and 5.8, one
+// token's 8-bit gate and up 8.8 and 9.4; but 2 x 4096 6.0 and 5.5, since every block rounds them all.
+constexpr int kRawRows = 8, kRawElements = 4096;
+
+// Quantising and the products in one launch: every block rounds the few rows of x for itself, into
+// shared memory.  (Asking for the first weights ahead of that: 6.9 us instead of 6.6.)
+template <bool GATED, bool F32>
+__global__ void __launch_bounds__(256, kResident) few_linear_kernel(const KArgs args, const RawRows raw) {
+  constexpr int V = 4;  // pieces of eight of a thread: rows of 4096 / x_rows elements need at most that
+  __shared__ uint4 xq[kRawElements / 16];  // [x_rows][pitch / 16]
+  __shared__ Used s;
+  __shared__ uint32_t big[kRawRows];
+  __shared__ float scale[kRawRows];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x < kRawRows) big[threadIdx.x] = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  KArgs a = args;
+  a.x = reinterpret_cast<const uint8_t*>(xq);
+  a.pitch = (a.k + 15) & ~15;
+  a.x_scale = scale;
+  // eight warps share the rows: one, two, four or eight to a row
+  const int to = a.x_rows > 4 ? 1 : a.x_rows > 2 ? 2 : a.x_rows > 1 ? 4 : 8;
+  const int row = warp / to, first = ((warp % to) * 32 + lane) * 8;
+  const bool mine = row < a.x_rows;
+  float v[V][8];
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (mine && first + j * to * 256 < a.pitch) raw8(raw, row, first + j * to * 256, a.k, v[j]);
+  find_used(a, s);  // a barrier at its end
+  if (mine) {
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (first + j * to * 256 < a.pitch)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) most = max(most, __float_as_uint(v[j][c]) & 0x7fffffffu);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) atomicMax(&big[row], most);
+  }
+  __syncthreads();
+  if (mine) {
+    const QuantScale qs = quant_scale(big[row]);
+    if (warp % to == 0 && lane == 0) scale[row] = qs.scale;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = first + j * to * 256;
+      if (i < a.pitch)
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(xq) + row * a.pitch + i) =
+            qs.inv == 0.f ? make_uint2(0, 0) : make_uint2(quant4(v[j], qs.inv), quant4(v[j] + 4, qs.inv));
+    }
+  }
+  __syncthreads();
+  few_items<true, GATED, F32>(a, s);
+}
+
+template <bool GATED>
+int few_blocks(const GroupedArgs& a) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return MSB_ECUDA;
+    return 0;
   const int64_t items = (int64_t)std::min(a.groups, a.out_rows) * (GATED ? a.n : (a.n + 1) / 2);
-  return launch_early(few_kernel<I8, GATED, F32>, std::min<int64_t>((items + 7) / 8, (int64_t)kResident * sms), 256, 0,
-                      st, k);
+  return (int)std::min<int64_t>((items + 7) / 8, (int64_t)kResident * sms);
+}
+template <bool I8, bool GATED, bool F32>
+int launch(const GroupedArgs& a, const KArgs& k, cudaStream_t st) {
+  const int blocks = few_blocks<GATED>(a);
+  return blocks ? launch_early(few_kernel<I8, GATED, F32>, blocks, 256, 0, st, k) : MSB_ECUDA;
+}
+template <bool GATED, bool F32>
+int launch_raw(const GroupedArgs& a, const KArgs& k, const RawRows& raw, cudaStream_t st) {
+  const int blocks = few_blocks<GATED>(a);
+  return blocks ? launch_early(few_linear_kernel<GATED, F32>, blocks, 256, 0, st, k, raw) : MSB_ECUDA;
 }
 
 }  // namespace
@@ -202,6 +304,20 @@ int launch_few(const GroupedArgs& a, const KArgs& k, cudaStream_t st) {
   if (a.swiglu) return a.i8 ? launch<true, true, false>(a, k, st) : launch<false, true, false>(a, k, st);
   if (a.i8) return a.out_f32 ? launch<true, false, true>(a, k, st) : launch<true, false, false>(a, k, st);
   return a.out_f32 ? launch<false, false, true>(a, k, st) : launch<false, false, false>(a, k, st);
+}
+
+int launch_linear(const GroupedArgs& a, const void* x, bool f32, int64_t ldx, int8_t* q, float* scale,
+                  cudaStream_t st) {
+  const int64_t pitch = ((int64_t)a.k + 15) & ~15;
+  if (few_rows(a) && a.x_rows > 0 && a.x_rows <= kRawRows && a.x_rows * pitch <= kRawElements) {
+    const bool by8 = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (a.x_rows == 1 || ldx % 8 == 0);
+    const RawRows raw = {x, ldx, f32, by8};
+    const KArgs k = kernel_args(a);
+    if (a.swiglu) return launch_raw<true, false>(a, k, raw, st);
+    return a.out_f32 ? launch_raw<false, true>(a, k, raw, st) : launch_raw<false, false>(a, k, raw, st);
+  }
+  const int rc = a.x_rows > 0 ? launch_quantize(x, f32, ldx, a.x_rows, a.k, q, a.ldx, scale, st) : MSB_OK;
+  return rc != MSB_OK ? rc : launch_grouped(a, st);
 }
 
 }  // namespace msb
