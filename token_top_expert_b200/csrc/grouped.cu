@@ -17,13 +17,16 @@
 //              two warps to a stage copy 16 bytes a thread, asynchronously, into the same
 //              swizzle, wait for them and hand the stage over.  (A gathering tensor-map load,
 //              four rows an instruction, took the copy unit 60 to 80 cycles for 512 bytes: gate
-//              and up of 4096 tokens 497 us, where the rest of the kernel took 254.)
+//              and up of 4096 tokens 497 us, where the rest of the kernel took 254.)  A copy costs three
+//              integer instructions: row pointers and swizzled places are kept per tile, and rows
+//              behind the tile's last are left out (with 23 a copy, long runs at the board's power
+//              limit took 262 us instead of 251, 8-bit ones 135 instead of 120).
 //
 // What bounds it: weights from memory while the groups are small (64 tokens' gate and up, hidden
 // 2048 x 768 channels x 128 experts top-8, 120 us for 0.79 GB: 6.6 TB/s), then the way from L2 to
 // the SMs, about 80 bytes per nanosecond and SM (a 256 x 256 tile's stage of 64 KB takes its pair
-// 430 ns, the matrix instructions 270 of them): 4096 tokens' gate and up 211 to 240 us, 0.86 to
-// 0.98 PFLOP/s; bf16 8192^3 575 to 600 us, 1.83 to 1.91 PFLOP/s.  Long runs meet the board's
+// 430 ns, the matrix instructions 270 of them): 4096 tokens' gate and up 205 to 250 us, 0.82 to
+// 1.0 PFLOP/s; bf16 8192^3 575 to 600 us, 1.83 to 1.91 PFLOP/s.  Long runs meet the board's
 // power limit and are slower by up to a fifth.
 #include <cuda.h>
 
@@ -756,8 +759,8 @@ int resident_clusters() {
 // Pairs that share the k of each tile of 64 rows: one group whose tiles are so few that the
 // device holds all their clusters at once, and enough stages that the join (two meetings of the
 // cluster and the parts' way through shared memory, 2 us) pays.  Without and with it, 64 rows: a
-// bf16 weight of 4096 x 4096 16.9 and 13.3 us, 512 x 4096 15.9 and 10.1, but 1024 x 1024 (16
-// stages) 7.2 and 8.0.
+// bf16 weight of 4096 x 4096 14.9 and 13.0 us, 512 x 4096 14.7 and 10.3, but 1024 x 1024 (16
+// stages) 6.8 and 8.1.
 int split_k(const GroupedArgs& a, const KArgs& k) {
   const int64_t tiles = ((int64_t)a.out_rows + 63) / 64 * k.mtiles, stages = (k.kbytes + kStageBytes - 1) / kStageBytes;
   if (a.groups != 1 || stages < 32) return 1;
@@ -769,13 +772,13 @@ int tile_rows(const GroupedArgs& a, const KArgs& k) {
   if (a.out_f32 && !a.i8) return 64;  // sums in registers
   const int64_t rows = a.out_rows, groups = std::min<int64_t>(a.groups, rows);
   // Few tiles: the smallest that one round of the pairs holds (one 4096 x 4096 bf16 weight, 64-,
-  // 128- and 256-row tiles: 256 rows 17.2, 23.1, 32.5 us; 512 rows 28.7, 23.1, 33.6; 1024 rows
-  // 51.7, 33.5, 31.4).
+  // 128- and 256-row tiles: 256 rows 15.5, 17.0, 25.3 us; 512 rows 25.9, 17.7, 26.0; 1024 rows
+  // 47.1, 31.0, 28.2).
   for (int bn = 64; bn <= 256; bn *= 2)
     if (k.mtiles * std::max(groups, (rows + bn - 1) / bn) <= kPairs) return bn;
   // Many: by the rows of a group, on average (gate and up of hidden 2048 x 768 channels x 128
-  // experts; bf16, 16 rows 120, 122, 128 us; 64 rows 148, 135, 138; 128 rows 240, 175, 157; 8
-  // bits, 16 rows 66, 67, 72; 64 rows 82, 75, 77; 128 rows 121, 92, 83).
+  // experts; bf16, 16 rows 126, 126, 132 us; 64 rows 144, 133, 137; 128 rows 216, 169, 153; 8
+  // bits, 16 rows 66, 68, 71; 64 rows 79, 71, 74; 128 rows 138, 92, 92).
   return rows <= 32 * groups ? 64 : rows <= 64 * groups ? 128 : 256;
 }
 

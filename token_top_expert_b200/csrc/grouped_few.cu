@@ -290,9 +290,9 @@ int launch_raw(const GroupedArgs& a, const KArgs& k, const RawRows& raw, cudaStr
 
 // Up to 8 rows (4 of one large weight), unless many weights have short rows, this kernel is the
 // faster one (the matrix unit's time in brackets, cold weights): one token's gate and up, hidden
-// 2048 x 768 channels x 128 experts top-8, 12.0 us (13.5), 8 bits 8.4 (9.1), but its 8-bit down
-// product with k = 768 9.8 (6.4); one 4096 x 4096 bf16 weight, 1 row 7.7 us (11.5), 4 rows 10.4
-// (11.6), 8 rows 16.2 (11.7); 1024 x 1024, 8 rows 5.4 (6.4).
+// 2048 x 768 channels x 128 experts top-8, 12.1 us (12.3), 8 bits 8.3 (8.8), but its 8-bit down
+// product with k = 768 9.9 (6.3); one 4096 x 4096 bf16 weight, 1 row 7.8 us (11.4), 4 rows 10.6
+// (11.6), 8 rows 16.6 (11.6); 1024 x 1024, 8 rows 5.6 (6.4).
 bool few_rows(const GroupedArgs& a) {
   const int64_t kbytes = (int64_t)a.k * (a.i8 ? 1 : 2);
   const int64_t bytes = std::min(a.groups, a.out_rows) * (a.swiglu ? 2 : 1) * kbytes * a.n;
