@@ -150,12 +150,16 @@ __device__ __forceinline__ void few_rows_of(const KArgs& a, const uint8_t* w0, c
 }
 
 // A warp takes two weight rows (gate and up of a channel, or two channels) at a time.
-template <bool I8, bool GATED, bool F32>
-__device__ __forceinline__ void few_items(const KArgs& a, const Used& s) {
+// SPREAD: `use` warps of a block do, else all eight (known to the compiler: it has no register left
+// for reading it, 1 row by 4096 x 4096 7.8 and 8.3 us).
+template <bool I8, bool GATED, bool F32, bool SPREAD>
+__device__ __forceinline__ void few_items(const KArgs& a, const Used& s, int use) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int each = GATED ? a.n : (a.n + 1) / 2;  // pairs of weight rows of a group
   const int64_t items = (int64_t)s.count * each;
-  for (int64_t item = (int64_t)blockIdx.x * 8 + warp; item < items; item += (int64_t)gridDim.x * 8) {
+  if (SPREAD && warp >= use) return;
+  const int warps = SPREAD ? use : 8;
+  for (int64_t item = (int64_t)blockIdx.x * warps + warp; item < items; item += (int64_t)gridDim.x * warps) {
     const int slot = (int)(item / each), ch = (int)(item - (int64_t)slot * each) * (GATED ? 1 : 2);
     const int group = s.group[slot], end = s.begin[group + 1];
     const uint8_t* const w0 = a.w + (int64_t)group * a.w_group + (int64_t)ch * a.w_n;
@@ -170,13 +174,13 @@ __device__ __forceinline__ void few_items(const KArgs& a, const Used& s) {
   }
 }
 
-template <bool I8, bool GATED, bool F32>
-__global__ void __launch_bounds__(256, kResident) few_kernel(const KArgs a) {
+template <bool I8, bool GATED, bool F32, bool SPREAD>
+__global__ void __launch_bounds__(256, kResident) few_kernel(const KArgs a, int use) {
   __shared__ Used s;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   find_used(a, s);
-  few_items<I8, GATED, F32>(a, s);
+  few_items<I8, GATED, F32, SPREAD>(a, s, use);
 }
 
 // Rows of x before they are quantised.  by8: eights of elements are 16-byte aligned.
@@ -217,7 +221,7 @@ constexpr int kRawRows = 8, kRawElements = 4096;
 // Quantising and the products in one launch: every block rounds the few rows of x for itself, into
 // shared memory.  (Asking for the first weights ahead of that: 6.9 us instead of 6.6.)
 template <bool GATED, bool F32>
-__global__ void __launch_bounds__(256, kResident) few_linear_kernel(const KArgs args, const RawRows raw) {
+__global__ void __launch_bounds__(256, kResident) few_linear_kernel(const KArgs args, const RawRows raw, int use) {
   constexpr int V = 4;  // pieces of eight of a thread: rows of 4096 / x_rows elements need at most that
   __shared__ uint4 xq[kRawElements / 16];  // [x_rows][pitch / 16]
   __shared__ Used s;
@@ -263,27 +267,36 @@ __global__ void __launch_bounds__(256, kResident) few_linear_kernel(const KArgs 
     }
   }
   __syncthreads();
-  few_items<true, GATED, F32>(a, s);
+  few_items<true, GATED, F32, true>(a, s, use);
 }
 
+// Blocks, and how many of a block's eight warps take items: all, but where the items would fill less
+// than half the blocks that the device holds, only so many that every block has some (8 and
+// fewer warps: 8 rows by 1024 x 1024 5.6 and 4.9 us, 4 rows by 2048 x 2048 6.2 and 5.6).
+struct Shape {
+  int blocks, use;
+};
 template <bool GATED>
-int few_blocks(const GroupedArgs& a) {
+Shape few_shape(const GroupedArgs& a) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
+    return {0, 0};
   const int64_t items = (int64_t)std::min(a.groups, a.out_rows) * (GATED ? a.n : (a.n + 1) / 2);
-  return (int)std::min<int64_t>((items + 7) / 8, (int64_t)kResident * sms);
+  const int64_t most = (int64_t)kResident * sms, use = items <= 4 * most ? (items + most - 1) / most : 8;
+  return {(int)std::min<int64_t>((items + use - 1) / use, most), (int)use};
 }
 template <bool I8, bool GATED, bool F32>
 int launch(const GroupedArgs& a, const KArgs& k, cudaStream_t st) {
-  const int blocks = few_blocks<GATED>(a);
-  return blocks ? launch_early(few_kernel<I8, GATED, F32>, blocks, 256, 0, st, k) : MSB_ECUDA;
+  const Shape s = few_shape<GATED>(a);
+  if (!s.blocks) return MSB_ECUDA;
+  return launch_early(s.use < 8 ? few_kernel<I8, GATED, F32, true> : few_kernel<I8, GATED, F32, false>, s.blocks, 256, 0,
+                      st, k, s.use);
 }
 template <bool GATED, bool F32>
 int launch_raw(const GroupedArgs& a, const KArgs& k, const RawRows& raw, cudaStream_t st) {
-  const int blocks = few_blocks<GATED>(a);
-  return blocks ? launch_early(few_linear_kernel<GATED, F32>, blocks, 256, 0, st, k, raw) : MSB_ECUDA;
+  const Shape s = few_shape<GATED>(a);
+  return s.blocks ? launch_early(few_linear_kernel<GATED, F32>, s.blocks, 256, 0, st, k, raw, s.use) : MSB_ECUDA;
 }
 
 }  // namespace
