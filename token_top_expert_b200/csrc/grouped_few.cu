@@ -301,15 +301,18 @@ int launch_raw(const GroupedArgs& a, const KArgs& k, const RawRows& raw, cudaStr
 
 }  // namespace
 
-// Up to 8 rows (4 of one large weight), unless many weights have short rows, this kernel is the
-// faster one (the matrix unit's time in brackets, cold weights): one token's gate and up, hidden
-// 2048 x 768 channels x 128 experts top-8, 12.1 us (12.3), 8 bits 8.3 (8.8), but its 8-bit down
-// product with k = 768 9.9 (6.3); one 4096 x 4096 bf16 weight, 1 row 7.8 us (11.4), 4 rows 10.6
-// (11.6), 8 rows 16.6 (11.6); 1024 x 1024, 8 rows 5.6 (6.4).
+// Up to 8 rows (4 of one weight that is large or has long rows), unless many weights have short rows,
+// this kernel is the faster one (the matrix unit's time in brackets, cold weights): one token's gate
+// and up, hidden 2048 x 768 channels x 128 experts top-8, 12.1 us (12.3), 8 bits 8.3 (8.8), but its
+// 8-bit down product with k = 768 9.9 (6.3).  One bf16 weight n x k: 4096 x 4096, 1 row 7.8 us (11.4),
+// 4 rows 10.6 (11.5), 8 rows 16.7 (11.6); 8 rows of 2048 x 2048 7.7 (8.1), 1024 x 1024 4.9 (6.3),
+// but 512 x 4096 10.9 (8.5).  8 bits: 8 rows of 2048 x 2048 5.5 (6.7), 4096 x 4096 9.0 (8.9), 6 rows
+// 7.9 (8.9).
 bool few_rows(const GroupedArgs& a) {
   const int64_t kbytes = (int64_t)a.k * (a.i8 ? 1 : 2);
   const int64_t bytes = std::min(a.groups, a.out_rows) * (a.swiglu ? 2 : 1) * kbytes * a.n;
-  if (a.w_k != 1 || a.out_rows > (a.groups > 1 || bytes <= 4 << 20 ? 8 : 4)) return false;
+  const bool small = kbytes <= 4096 && bytes <= (a.i8 ? 16 : 8) << 20;
+  if (a.w_k != 1 || a.out_rows > (a.groups > 1 || small ? 8 : 4)) return false;
   return kbytes >= 1024 || bytes <= 1 << 20;
 }
 
