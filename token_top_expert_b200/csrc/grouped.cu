@@ -17,13 +17,14 @@
 //              two warps to a stage copy 16 bytes a thread, asynchronously, into the same
 //              swizzle, wait for them and hand the stage over.  (A gathering tensor-map load,
 //              four rows an instruction, took the copy unit 60 to 80 cycles for 512 bytes: gate
-//              and up of 4096 tokens 497 us, where the rest of the kernel took 254.)  A copy costs three
-//              integer instructions: row pointers and swizzled places are kept per tile, and rows
-//              behind the tile's last are left out (with 23 a copy, long runs at the board's power
-//              limit took 262 us instead of 251, 8-bit ones 135 instead of 120).
+//              and up of 4096 tokens 497 us, where the rest of the kernel took 254.)  Row pointers and
+//              swizzled places are kept per tile, and rows behind the tile's last are left out: the
+//              kernel's instructions for 4096 tokens' gate and up went from 86 to 67 million (in
+//              order: 27), long runs at the board's power limit from 262 to 251 us, 8-bit ones from
+//              135 to 120.
 //
 // What bounds it: weights from memory while the groups are small (64 tokens' gate and up, hidden
-// 2048 x 768 channels x 128 experts top-8, 120 us for 0.79 GB: 6.6 TB/s), then the way from L2 to
+// 2048 x 768 channels x 128 experts top-8, 96 to 120 us for 0.8 GB), then the way from L2 to
 // the SMs, about 80 bytes per nanosecond and SM (a 256 x 256 tile's stage of 64 KB takes its pair
 // 430 ns, the matrix instructions 270 of them): 4096 tokens' gate and up 205 to 250 us, 0.82 to
 // 1.0 PFLOP/s; bf16 8192^3 575 to 600 us, 1.83 to 1.91 PFLOP/s.  Long runs meet the board's
@@ -95,11 +96,14 @@ struct RowMaps {
 };
 
 // A bounded wait.  When it runs out, or another role of this CTA has given up, the caller
-// stops waiting for good and leaves through the common exit.
+// stops waiting for good and leaves through the common exit.  A poll may sleep up to kNapNs (it
+// ends with the phase all the same): with the default, far shorter one the waiting warps' polls
+// took issue slots (64 tokens' gate and up 98.0 us, 96.0 with it; 256 x 4096 by 4096 x 4096 15.6 and 14.1).
+constexpr uint32_t kNapNs = 5000;
 __device__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t* dead) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1; i < kSpinLimit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_sleep(bar, parity, kNapNs)) return true;
     if (*(volatile uint32_t*)dead) return false;
     if ((i & 15u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) break;
   }
@@ -108,7 +112,7 @@ __device__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t* dead) {
   return false;
 }
 __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, uint32_t* dead) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, dead);
+  return mbar_try_wait_sleep(bar, parity, kNapNs) || wait_slow(bar, parity, dead);
 }
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint32_t* dead) {
   return __all_sync(0xffffffffu, wait_one(bar, parity, dead));
