@@ -18,10 +18,10 @@
 //              swizzle, wait for them and hand the stage over.  (A gathering tensor-map load,
 //              four rows an instruction, took the copy unit 60 to 80 cycles for 512 bytes: gate
 //              and up of 4096 tokens 497 us, where the rest of the kernel took 254.)  Row pointers and
-//              swizzled places are kept per tile, and rows behind the tile's last are left out: the
-//              kernel's instructions for 4096 tokens' gate and up went from 86 to 67 million (in
-//              order: 27), long runs at the board's power limit from 262 to 251 us, 8-bit ones from
-//              135 to 120.
+//              swizzled places are kept per tile, rows behind the tile's last are left out, and only the
+//              last stage and rows outside x have a size of their own: the kernel's instructions for
+//              4096 tokens' gate and up went from 86 to 55 million (in order: 26), long runs at the
+//              board's power limit from 262 to 250 us, 8-bit ones from 135 to 120.
 //
 // What bounds it: weights from memory while the groups are small (64 tokens' gate and up, hidden
 // 2048 x 768 channels x 128 experts top-8, 96 to 120 us for 0.8 GB), then the way from L2 to
@@ -535,20 +535,21 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(Cfg<BN>::kTh
       for (; i < nk; i += kStages) {
         if (!(ok = wait_warp(&s.empty[st], phase ^ 1, &s.dead))) break;
         phase ^= 1;
-        const int left = a.kbytes - (kb + i) * kStageBytes - chunk * 16;
-        const uint32_t valid = left < 0 ? 0 : left > 16 ? 16 : left;
-        const uint32_t k0 = valid ? (kb + i) * kStageBytes : 0;
+        const uint32_t k0 = (kb + i) * kStageBytes;
         const uint32_t even = dst + ((chunk ^ r0) << 4), odd = dst + ((chunk ^ (4 + r0)) << 4);
-        if (all) {
+        if (all && (int)k0 + kStageBytes <= a.kbytes) {
 #pragma unroll
           for (int q = 0; q < C::kLaneRows; ++q)
-            if (q * 4 < rows) cp_async16((q & 1 ? odd : even) + q * 4 * kStageBytes, src[q] + k0, valid);
-        } else {  // zeros for rows outside x
+            if (q * 4 < rows) cp_async16((q & 1 ? odd : even) + q * 4 * kStageBytes, src[q] + k0);
+        } else {  // zeros for rows outside x and behind the end of k
+          const int left = a.kbytes - (int)k0 - chunk * 16;
+          const uint32_t valid = left < 0 ? 0 : left > 16 ? 16 : left;
 #pragma unroll
           for (int q = 0; q < C::kLaneRows; ++q)
-            if (q * 4 < rows)
-              cp_async16((q & 1 ? odd : even) + q * 4 * kStageBytes, src[q] + (there >> q & 1 ? k0 : 0),
-                         there >> q & 1 ? valid : 0);
+            if (q * 4 < rows) {
+              const uint32_t size = there >> q & 1 ? valid : 0;
+              cp_async16((q & 1 ? odd : even) + q * 4 * kStageBytes, src[q] + (size ? k0 : 0), size);
+            }
         }
         cp_async_wait_all();
         fence_proxy_async();

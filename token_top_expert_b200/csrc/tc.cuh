@@ -144,7 +144,11 @@ __device__ __forceinline__ void prefetch_map(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-// 16 bytes global -> shared, the bytes past `valid` (0..16) zero-filled and not read.
+// 16 bytes global -> shared.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The bytes past `valid` (0..16) zero-filled and not read.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid)
                : "memory");
