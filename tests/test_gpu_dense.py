@@ -669,6 +669,30 @@ def test_dense_block_padded_and_int8(msb):
     assert (y8[~mask] == 0).all()
 
 
+@pytest.mark.parametrize("tokens", [1, 2, 9])
+def test_dense_block_int8_is_its_parts(msb, tokens):
+    """The 8-bit block bit for bit as its operators one after the other, eager and replayed."""
+    import torch
+    w = synth.QWEN30B_BLOCK
+    layer = msb.Int8Layer.from_packed(device_layer(w, rank=0))
+    x = to_bf16_tensor(synth.activations(w, 7, batch=tokens))
+    router = layer.router_t.view(torch.bfloat16).view(w.experts, w.d)
+    r = msb.route(msb.grouped_matmul(x, router, out_dtype=torch.float32), w.top_e, renorm=bool(layer.dims.renorm))
+    h = msb.swiglu_int8(x, layer.gate_up, layer.gate_up_scale, r.offsets, rows=r.rows)
+    y = msb.linear_int8(h, layer.down[..., :w.inter], layer.down_scale, r.offsets)
+    want = msb.combine(y, r)
+    assert torch.equal(msb.moe_dense_block(x, layer), want)
+    out, space = torch.empty_like(x), msb.DenseWorkspace(layer.dims, tokens, int8=True)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        msb.moe_dense_block(x, layer, out=out, workspace=space)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+    msb.dense_check()
+
+
 def test_prompt_step_with_norms_captured(msb):
     """Two layers of a stack, block_norm around moe_dense_block, as a user runs them: eager and
     replayed from a graph on another stream, the same bits; a second graph beside it does not
