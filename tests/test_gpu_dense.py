@@ -542,6 +542,29 @@ def test_combine(msb, d):
         assert (got[3] == 0).all()
 
 
+@pytest.mark.parametrize("T,K", [(1185, 1), (2369, 2), (1191, 3), (1300, 4), (1201, 5), (1184, 9), (2400, 16)])
+@pytest.mark.parametrize("d", [8, 2056])
+def test_combine_many_tokens(msb, T, K, d):
+    """Blocks that take several tokens: as test_combine, pitches wider than the rows, rows left out."""
+    import torch
+    R = 500
+    pos = torch.randint(-1, R + 1, (T, K), device="cuda", dtype=torch.int32)
+    w = rnd(29, T, K, dtype=torch.float32)
+    r = msb.Routing(None, w, None, None, pos)
+    ok = (pos >= 0) & (pos < R)
+    for dtype in (torch.bfloat16, torch.float32):
+        y = rnd(30, R, d + 8, dtype=dtype)[:, :d]
+        want, mag = torch.zeros(T, d, device="cuda", dtype=torch.float64), torch.zeros(T, d, device="cuda", dtype=torch.float64)
+        for k in range(K):
+            term = torch.where(ok[:, k], w[:, k], 0.0).double()[:, None] * y.double()[pos[:, k].long().clamp(0, R - 1)]
+            want += term
+            mag += term.abs()
+        out = torch.full((T + 1, d + 16), 3.0, device="cuda", dtype=torch.bfloat16)
+        got = msb.combine(y, r, out=out[:T, :d])
+        within(got, want, BF16 * want.abs() + (K + 1) * F32 * mag + TINY)
+        assert (out[T] == 3).all() and (out[:, d:] == 3).all()
+
+
 # ------------------------------------------------------------------ block norm
 
 @pytest.mark.parametrize("R,d", [(1, 1), (4, 64), (3, 433), (70, 1000), (5, 2048), (9, 4096), (2, 8192), (2, 16384)])
