@@ -256,3 +256,35 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         msb.Int8Layer(msb.Dims(64, 16, 2, 1, 0), torch.zeros(2, 2, 16, 64), torch.zeros(2, 2, 16),
                       torch.zeros(2, 64, 16), torch.zeros(2, 64), torch.zeros(2, 64, dtype=bf))
+
+
+def test_gate_offsets_pass_32_bits(tmp_path):
+    """Offsets of strided gates in 64 bits at every size that the checks admit: the kernels' own
+    expression (csrc/dense.h), compiled for the host."""
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "gate.cpp"
+    src.write_text(r"""
+#include "dense.h"
+int main() {
+  msb::NormArgs a = {};
+  const int64_t strides[] = {0, 1, 3, 1 << 22, 1 << 23, 1 << 26, (1 << 28) - 1};
+  const int rows[] = {0, 1, 255, 256, 16383, 0x7ffffffe};
+  for (int64_t row : strides)
+    for (int64_t col : strides)
+      for (int t : rows)
+        for (int i : rows) {
+          if (i >= MSB_NORM_MAX_D) continue;
+          a.gate_row = row, a.gate_col = col;
+          const __int128 want = (__int128)t * row + (__int128)i * col;
+          if (a.gate_at(t, i) != want) return 1;
+        }
+  return 0;
+}
+""")
+    exe = str(tmp_path / "gate")
+    subprocess.run(["g++", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I", os.path.join(root, "include"),
+                    "-I", os.path.join(root, "token_top_expert_b200", "csrc"), "-I", "/usr/local/cuda/include",
+                    str(src), "-o", exe], check=True)
+    subprocess.run([exe], check=True)

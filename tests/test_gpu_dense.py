@@ -638,6 +638,51 @@ def test_block_norm_special_rows(msb):
     assert torch.isinf(ho[2, 9].float()) and torch.isnan(x[2, 9].float()) and (x[2, :9] == 0).all()
 
 
+@pytest.mark.parametrize("R,d", [(3, 40), (5, 33), (4, 433), (3, 1000), (6, 1001), (3, 2048), (5, 4097), (1500, 264), (2, 16384)])
+@pytest.mark.parametrize("h32", [True, False])
+def test_block_norm_strided_gates(msb, R, d, h32):
+    """A gate of any strides (transposed, every third column, one row or column of a matrix) gives
+    the bits of its contiguous copy: the same steps on the same values.  What lies between is NaN."""
+    import torch
+    h, y = rnd(80, R, d, dtype=torch.float32 if h32 else None), rnd(81, R, d)
+    pre, pw = rnd(82, d), rnd(83, d)
+
+    def views(dtype):
+        nan = lambda *s: torch.full(s, float("nan"), device="cuda", dtype=dtype)  # noqa: E731
+        g = rnd(84, R, d, dtype=dtype)
+        b = nan(d, R + 3)
+        yield "transposed", g, b[:, 1:R + 1].t()
+        b = nan(R, 3 * d + 5)
+        yield "every third", g, b[:, 2:2 + 3 * d:3]
+        yield "one row", g[:1], nan(d, 7)[:, 2:3].t()
+        yield "channel", g[0], nan(d, 5)[:, 3]
+        yield "token", g[:, :1], nan(R, 9)[:, 4:5]
+
+    for dtype in (torch.bfloat16, torch.float32):
+        for name, g, v in views(dtype):
+            v.copy_(g)
+            kw = dict(pre_weight=pre, post_norm=True, post_weight=pw, skip_scale=0.5, residual_scale=0.22)
+            want = msb.block_norm(h, y, h_out=torch.empty_like(h), gate=g.contiguous(), **kw)
+            got = msb.block_norm(h, y, h_out=torch.empty_like(h), gate=v, **kw)
+            assert torch.isfinite(want[0]).all()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (name, dtype)
+
+
+@pytest.mark.parametrize("d,stride", [(33, 1 << 26), (513, 1 << 23)])
+def test_block_norm_gate_columns_far_apart(msb, d, stride):
+    """Columns of a transposed gate 2^23 and 2^26 elements apart: their offsets pass 32 bits."""
+    import torch
+    R = 2
+    buf = torch.empty((d, stride), device="cuda", dtype=torch.bfloat16)
+    gate = buf.t()[:R]
+    g = rnd(85, R, d)
+    gate.copy_(g)
+    h, y = rnd(86, R, d), rnd(87, R, d)
+    want = msb.block_norm(h, y, h_out=torch.empty_like(h), gate=g)
+    got = msb.block_norm(h, y, h_out=torch.empty_like(h), gate=gate)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ------------------------------------------------------------------ the block
 
 @pytest.mark.parametrize("tokens", [1, 3, 300])

@@ -47,6 +47,10 @@ struct NormArgs {
   int rows, d;
   bool h_f32, y_f32, w_f32, gate_f32, post_norm;
   float skip, residual, eps, inv_d;
+
+  // Where element (t, i) of the gate lies, in elements.  Strides reach 2^28: a column's offset
+  // alone passes 32 bits.
+  __host__ __device__ int64_t gate_at(int64_t t, int64_t i) const { return t * gate_row + i * gate_col; }
 };
 int launch_block_norm(const NormArgs& a, cudaStream_t st);
 

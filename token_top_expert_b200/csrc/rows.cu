@@ -464,11 +464,11 @@ __global__ void __launch_bounds__(block_threads(NT)) block_norm_any_kernel(const
 #pragma unroll
       for (int j = 0; j < V; ++j) y[j] *= g;
     } else if (a.gate) {
-      const uint8_t* const g = from(a.gate, a.gate_f32, t * a.gate_row + tid * a.gate_col);
-      const int step = NT * (int)a.gate_col;
+      const uint8_t* const g = from(a.gate, a.gate_f32, a.gate_at(t, tid));
 #pragma unroll
       for (int j = 0; j < V; ++j)
-        if (j * NT < here) y[j] *= a.gate_col == 1 ? at(g, a.gate_f32, j * NT) : load(g, a.gate_f32, (int64_t)j * step);
+        if (j * NT < here)
+          y[j] *= a.gate_col == 1 ? at(g, a.gate_f32, j * NT) : load(g, a.gate_f32, a.gate_at(0, j * NT));
     }
   }
   float ss = 0.f;
