@@ -18,8 +18,9 @@
  *
  * Conventions are those of msb.h (device pointers of the current device, caller-owned
  * buffers, asynchronous on `stream`, MSB_OK or a negative code, argument errors before
- * anything is enqueued).  Row pitches are in elements, 0 .. 2^28 - 1.  Nothing here keeps state between calls except one error word per
- * device, set when a bounded wait inside a kernel runs out: msb_dense_check reads it.
+ * anything is enqueued).  Row pitches are in elements, 0 .. 2^28 - 1.  Nothing here keeps
+ * state between calls except one error word per device, set when a bounded wait inside a
+ * kernel runs out: msb_dense_check reads it.
  * Calls may overlap on the GPU (other streams, captured graphs) as long as their output and
  * workspace buffers differ.
  */
@@ -115,7 +116,8 @@ int32_t msb_grouped_swiglu(const void* x, int64_t ldx, int32_t x_rows, const int
  * (FP32 steps, ties to even).  A row whose largest magnitude is below 2^-119 becomes zeros
  * with scale 0; a row with a NaN or infinity becomes zeros with scale NaN.
  *  x        x_type (MSB_BF16 or MSB_F32), rows ldx elements apart.
- *  q        int8, rows ldq bytes apart (ldq >= k); scale float [rows]. */
+ *  q        int8, rows ldq bytes apart (ldq >= k); scale float [rows].
+ *  rows 0..; k 1..2^28 - 1. */
 int32_t msb_int8_quantize(const void* x, int32_t x_type, int64_t ldx, int32_t rows, int32_t k,
                           int8_t* q, int64_t ldq, float* scale, void* stream);
 
@@ -147,7 +149,9 @@ int32_t msb_int8_linear(const void* x, int32_t x_type, int64_t ldx, int32_t x_ro
  * out[t] = sum over k of weights[t][k] * y[pos[t][k]], in the order of k, in FP32, rounded
  * once; pairs whose pos is outside 0..y_rows-1 are left out (a token without any: zeros).
  *  y        y_type (MSB_BF16 or MSB_F32) [y_rows], rows ldy elements apart.
- *  out      bf16 [tokens], rows ldo elements apart; must not overlap y. */
+ *  out      bf16 [tokens], rows ldo elements apart; must not overlap y.
+ *  tokens 0..; top_e, d 1..2^28 - 1, and below 2^31 blocks: tokens * ceil(d / 256) < 2^31 is
+ *  enough (MSB_EUNSUPPORTED else). */
 int32_t msb_combine(const void* y, int32_t y_type, int64_t ldy, int32_t y_rows, const int32_t* pos,
                     const float* weights, int32_t tokens, int32_t top_e, int32_t d, void* out,
                     int64_t ldo, void* stream);

@@ -288,3 +288,14 @@ int main() {
                     "-I", os.path.join(root, "token_top_expert_b200", "csrc"), "-I", "/usr/local/cuda/include",
                     str(src), "-o", exe], check=True)
     subprocess.run([exe], check=True)
+
+
+def test_row_lengths_have_a_limit(lib, st):
+    """Lengths from 2^28 on, whose 32-bit steps along a row would wrap, are refused before any
+    launch (one row: its pitch says nothing)."""
+    for k in (1 << 28, (1 << 31) - 300, (1 << 31) - 1):
+        assert lib.msb_int8_quantize(A, 0, 0, 1, k, B, 0, 2 * B, None) == st.MSB_EUNSUPPORTED
+        assert lib.msb_combine(A, 0, 0, 1, B, 2 * B, 1, 1, k, 3 * B, 0, None) == st.MSB_EUNSUPPORTED
+        assert lib.msb_combine(A, 0, 0, 1, B, 2 * B, 1, k, 8, 3 * B, 0, None) == st.MSB_EUNSUPPORTED
+    # as many (token, run of columns) items as a launch cannot hold
+    assert lib.msb_combine(A, 0, 0, 1, B, 2 * B, 1 << 30, 1, 1 << 20, 3 * B, 1 << 20, None) == st.MSB_EUNSUPPORTED

@@ -565,6 +565,24 @@ def test_combine_many_tokens(msb, T, K, d):
         assert (out[T] == 3).all() and (out[:, d:] == 3).all()
 
 
+def test_longest_rows(msb):
+    """Rows of 2^28 - 1 (and - 8) elements, the longest that are taken: bit for bit."""
+    import torch
+    d = (1 << 28) - 8
+    y = rnd(88, 2, d)
+    w = torch.tensor([[0.5, 2.0]], device="cuda")
+    r = msb.Routing(None, w, None, None, torch.tensor([[1, 0]], device="cuda", dtype=torch.int32))
+    got = msb.combine(y, r)
+    # powers of two: the products are exact, the sum is rounded once to float and once to bf16
+    assert torch.equal(got[0], (0.5 * y[1].float() + 2.0 * y[0].float()).bfloat16())
+    k = (1 << 28) - 1
+    x = y.view(-1)[:k].view(1, k)
+    x[0, 5] = 16.0  # the maximum: 127 / 16 is exact
+    q, s = msb.quantize_int8(x)
+    assert abs(float(s[0]) - 16.0 / 127.0) <= F32 * 16.0 / 127.0
+    assert torch.equal(q[0], torch.round(x[0].float() * (127.0 / 16.0)).to(torch.int8))
+
+
 # ------------------------------------------------------------------ block norm
 
 @pytest.mark.parametrize("R,d", [(1, 1), (4, 64), (3, 433), (70, 1000), (5, 2048), (9, 4096), (2, 8192), (2, 16384)])

@@ -37,6 +37,8 @@ bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
 }
 // A row pitch in elements that the byte arithmetic of a call can take (2^31 rows, 4 bytes).
 bool pitch_ok(int64_t ld) { return ld >= 0 && ld < (int64_t)1 << 28; }
+// A row length (or experts of a token) that the kernels' 32-bit steps along it can take.
+bool length_ok(int32_t n) { return n < 1 << 28; }
 
 // Checks the arguments of a grouped product and completes `a`; MSB_OK with a.out_rows = 0 means
 // that there is nothing to do.
@@ -264,6 +266,7 @@ int32_t msb_int8_quantize(const void* x, int32_t x_type, int64_t ldx, int32_t ro
   if (rows < 0 || k < 1 || !type_ok(x_type) || !pitch_ok(ldx) || !pitch_ok(ldq) ||
       (rows > 1 && ldq < k) || (rows > 0 && (!x || !q || !scale)))
     return MSB_EINVAL;
+  if (!length_ok(k)) return MSB_EUNSUPPORTED;
   if (!aligned(x, size_of(x_type)) || !aligned(scale, 4)) return MSB_EINVAL;
   if (overlaps(x, extent(rows, ldx, k, size_of(x_type)), q, extent(rows, ldq, k, 1)) ||
       overlaps(scale, 4 * (int64_t)rows, q, extent(rows, ldq, k, 1)) ||
@@ -328,6 +331,7 @@ int32_t msb_combine(const void* y, int32_t y_type, int64_t ldy, int32_t y_rows, 
   if (tokens < 0 || top_e < 1 || d < 1 || y_rows < 0 || !type_ok(y_type) || !pitch_ok(ldy) ||
       !pitch_ok(ldo) || (tokens > 1 && ldo < d))
     return MSB_EINVAL;
+  if (!length_ok(d) || !length_ok(top_e)) return MSB_EUNSUPPORTED;
   if (tokens > 0 && (!pos || !weights || !out || (y_rows > 0 && !y))) return MSB_EINVAL;
   if (!aligned4({pos, weights}) || !aligned(y, size_of(y_type)) || !aligned(out, 2)) return MSB_EINVAL;
   if (overlaps(y, extent(y_rows, ldy, d, size_of(y_type)), out, extent(tokens, ldo, d, 2)))
