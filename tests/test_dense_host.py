@@ -299,3 +299,16 @@ def test_row_lengths_have_a_limit(lib, st):
         assert lib.msb_combine(A, 0, 0, 1, B, 2 * B, 1, k, 8, 3 * B, 0, None) == st.MSB_EUNSUPPORTED
     # as many (token, run of columns) items as a launch cannot hold
     assert lib.msb_combine(A, 0, 0, 1, B, 2 * B, 1 << 30, 1, 1 << 20, 3 * B, 1 << 20, None) == st.MSB_EUNSUPPORTED
+
+
+def test_swiglu_int8_has_no_float_output():
+    """SwiGLU products are bf16: another out_dtype is refused, as an `out` of another type is."""
+    import torch
+
+    import token_top_expert_b200 as msb
+    q, w = torch.zeros(6, 32, dtype=torch.int8), torch.zeros(2, 2, 8, 32, dtype=torch.int8)
+    offs, qs, ws = torch.zeros(3, dtype=torch.int32), torch.zeros(6), torch.zeros(2, 2, 8)
+    for kw in (dict(out_dtype=torch.float32), dict(out_dtype=torch.float16),
+               dict(out=torch.zeros(6, 8, dtype=torch.bfloat16), out_dtype=torch.float32), dict(out=torch.zeros(6, 8))):
+        with pytest.raises(ValueError, match="SwiGLU|float16|out_dtype"):
+            msb.matmul_int8(q, qs, w, ws, offs, swiglu=True, **kw)

@@ -311,9 +311,8 @@ def matmul_int8(q, q_scale, w, w_scale, offsets=None, rows=None, out=None, out_d
                 swiglu: bool = False, stream=None):
     """grouped_matmul (or grouped_swiglu) on 8-bit integers: q int8 [rows][k] with q_scale
     float32 [rows], w int8 like the bf16 weights (k contiguous) with w_scale float32 of w's
-    shape without k."""
-    return _product("matmul_int8", q, w, offsets, rows, out, None if swiglu else out_dtype, stream, swiglu,
-                    q_scale, w_scale)
+    shape without k.  SwiGLU products are bf16."""
+    return _product("matmul_int8", q, w, offsets, rows, out, out_dtype, stream, swiglu, q_scale, w_scale)
 
 
 def linear_int8(x, w, w_scale, offsets=None, rows=None, out=None, out_dtype=None, stream=None):
