@@ -137,7 +137,8 @@ int32_t msb_int8_swiglu(const int8_t* q, int64_t ldq, const float* q_scale, int3
 
 /* msb_int8_quantize of x, then msb_int8_matmul (swiglu = 0) or msb_int8_swiglu (swiglu = 1,
  * out_type MSB_BF16): the same results.  workspace: msb_int8_linear_workspace_size(x_rows, k)
- * bytes (at least 16; 0 for sizes out of range), 16-byte aligned, no initial contents needed. */
+ * bytes (at least 16; 0 for sizes out of range), 16-byte aligned, no initial contents needed;
+ * must not overlap x or out. */
 size_t msb_int8_linear_workspace_size(int32_t x_rows, int32_t k);
 int32_t msb_int8_linear(const void* x, int32_t x_type, int64_t ldx, int32_t x_rows,
                         const int32_t* rows, const int32_t* offsets, int32_t groups,

@@ -312,3 +312,16 @@ def test_swiglu_int8_has_no_float_output():
                dict(out=torch.zeros(6, 8, dtype=torch.bfloat16), out_dtype=torch.float32), dict(out=torch.zeros(6, 8))):
         with pytest.raises(ValueError, match="SwiGLU|float16|out_dtype"):
             msb.matmul_int8(q, qs, w, ws, offs, swiglu=True, **kw)
+
+
+def test_int8_linear_scratch_and_out_are_apart(lib, st):
+    """out must miss the whole workspace, the rows' scales at its end too."""
+    nb = lib.msb_int8_linear_workspace_size(10, 100)
+    w = weights(st, stride_n=112)
+
+    def call(out):
+        return lib.msb_int8_linear(B, 0, 100, 10, None, None, 1, 10, ctypes.byref(w), A, 64, 100, 0, out, 0, 64,
+                                   3 * B, nb, None)
+    scales = 3 * B + 10 * 112
+    for out in (scales, scales + 36, 3 * B - 64, 3 * B + 4):
+        assert call(out) == st.MSB_EINVAL, out - 3 * B

@@ -314,7 +314,9 @@ int32_t msb_int8_linear(const void* x, int32_t x_type, int64_t ldx, int32_t x_ro
   if (k > MSB_INT8_MAX_K) return MSB_EUNSUPPORTED;
   const int64_t need = (int64_t)msb_int8_linear_workspace_size(x_rows, k), pitch = ((int64_t)k + 15) & ~15;
   const int64_t xb = extent(x_rows, ldx, k, size_of(x_type)), ob = extent(out_rows, ldo, n, size_of(out_type));
-  if (workspace_bytes < (size_t)need || overlaps(workspace, need, x, xb) || overlaps(out, ob, x, xb)) return MSB_EINVAL;
+  if (workspace_bytes < (size_t)need || overlaps(workspace, need, x, xb) || overlaps(out, ob, x, xb) ||
+      overlaps(out, ob, workspace, need))
+    return MSB_EINVAL;
   int8_t* const q = static_cast<int8_t*>(workspace);
   float* const scale = reinterpret_cast<float*>(q + x_rows * pitch);
   GroupedArgs a = grouped_args(q, pitch, x_rows, rows, offsets, groups, out_rows, n, k, out, ldo);
