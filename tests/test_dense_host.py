@@ -325,3 +325,16 @@ def test_int8_linear_scratch_and_out_are_apart(lib, st):
     scales = 3 * B + 10 * 112
     for out in (scales, scales + 36, 3 * B - 64, 3 * B + 4):
         assert call(out) == st.MSB_EINVAL, out - 3 * B
+
+
+def test_workspaces_lie_in_a_row():
+    """A workspace with gaps between its elements is refused: scratch is written byte after byte."""
+    import torch
+
+    import token_top_expert_b200 as msb
+    gaps = torch.zeros(1 << 16, dtype=torch.uint8)[::2]
+    x, w = torch.zeros(6, 32, dtype=torch.bfloat16), torch.zeros(8, 32, dtype=torch.int8)
+    for f in (lambda ws: msb.linear_int8(x, w, torch.zeros(8), workspace=ws),
+              lambda ws: msb.swiglu_int8(x, w[None].expand(2, 8, 32).contiguous(), torch.zeros(2, 8), workspace=ws)):
+        with pytest.raises(ValueError, match="contiguous"):
+            f(gaps)

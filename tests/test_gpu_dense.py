@@ -459,6 +459,39 @@ def test_linear_int8_is_quantize_and_matmul(msb, R, k, f32, lead, pitch):
                 msb.matmul_int8(q, qs, w, ws, offs, rows=rows, swiglu=True))
 
 
+@pytest.mark.parametrize("R", [2, 700])
+def test_linear_int8_with_scratch_of_the_caller(msb, R):
+    """out and workspace given: the same bits, on a raw stream handle too; nothing behind the
+    workspace is written; one that is too small is refused."""
+    import torch
+    n, k, E = 96, 520, 3
+    x = rnd(90, R, k)
+    w = torch.randint(-127, 128, (E, 2, n, 528), device="cuda").to(torch.int8)[..., :k]
+    ws = rnd(91, E, 2, n, dtype=torch.float32).abs() * 1e-3
+    rows = torch.arange(R, device="cuda", dtype=torch.int32)
+    offs = offsets_of([R // 2, 0, R - R // 2])
+    need = msb.load_library().msb_int8_linear_workspace_size(R, k)
+    buf = torch.full((need + 64,), 7, device="cuda", dtype=torch.uint8)
+    side = torch.cuda.Stream()
+    for f, at, kw in ((msb.linear_int8, (w[1, 0], ws[1, 0]), {}), (msb.swiglu_int8, (w, ws, offs), dict(rows=rows))):
+        want = f(x, *at, **kw)
+        out = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        for stream in (None, side, side.cuda_stream):
+            out.zero_()
+            torch.cuda.synchronize()
+            assert f(x, *at, out=out, workspace=buf[:need], stream=stream, **kw) is out
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+        assert (buf[need:] == 7).all()
+        with pytest.raises(msb.MsbError):
+            f(x, *at, out=out, workspace=buf[:need - 1], **kw)
+        with pytest.raises(ValueError):
+            f(x, *at, out=out, stream=side.cuda_stream, **kw)
+        with pytest.raises(ValueError):
+            f(x, *at, out=out, workspace=torch.zeros(need, dtype=torch.uint8), **kw)
+
+
 # ------------------------------------------------------------------ routing
 
 def route_ref(l, top_e, renorm, mask):

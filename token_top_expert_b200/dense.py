@@ -96,6 +96,13 @@ def _floats(t, shape, what: str):
                          % (what, tuple(shape), t.dtype, tuple(t.shape)))
 
 
+def _scratch(t):
+    """(address, bytes) of a caller's workspace, whose bytes must lie in a row."""
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous, got strides %s" % (t.stride(),))
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def dense_check(stream=None):
     """Raise MsbError if a kernel of this module's calls on the current device was flagged
     since the last check (synchronises the stream)."""
@@ -202,8 +209,9 @@ def _weights(w, parts: bool):
     return MsbGroupWeights(w.data_ptr(), stride[0], stride[1] if parts else 0, sn, sk), shape[0], n, k
 
 
-def _product(what, x, w, offsets, rows, out, out_dtype, stream, parts, q_scale=None, w_scale=None, q=None):
-    """One grouped product.  q: quantise x on the way (None: x is what is multiplied)."""
+def _product(what, x, w, offsets, rows, out, out_dtype, stream, parts, q_scale=None, w_scale=None, q=None,
+             workspace=None):
+    """One grouped product.  q: quantise x on the way (None: x is what is multiplied), in `workspace`."""
     import torch
     i8 = w_scale is not None
     gw, groups, n, k = _weights(w, parts)
@@ -234,7 +242,8 @@ def _product(what, x, w, offsets, rows, out, out_dtype, stream, parts, q_scale=N
     code = _type(out, "out")
     if parts and code != _lib.MSB_BF16:
         raise ValueError("SwiGLU products are bf16")
-    dev = _here(x, w, offsets, rows, out, q_scale, w_scale)
+    given = None if workspace is None else _scratch(workspace)
+    dev = _here(x, w, offsets, rows, out, q_scale, w_scale, workspace)
     off, row, o = _ptr(offsets), _ptr(rows), out.data_ptr()
     lib = _lib.load()
     if not i8:
@@ -253,10 +262,12 @@ def _product(what, x, w, offsets, rows, out, out_dtype, stream, parts, q_scale=N
             nb = _linear_bytes(R, k)
             if nb == 0:
                 raise ValueError("x of %d rows of %d is beyond the library's limits" % (R, k))
-            ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
-            new.append(ws)
+            if workspace is None:
+                ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
+                new.append(ws)
+                given = ws.data_ptr(), nb
             rc = lib.msb_int8_linear(x.data_ptr(), _type(x, "x"), ldx, R, row, off, groups, r, gw,
-                                     w_scale.data_ptr(), n, k, 1 if parts else 0, o, code, ldo, ws.data_ptr(), nb,
+                                     w_scale.data_ptr(), n, k, 1 if parts else 0, o, code, ldo, *given,
                                      _on(stream, dev, new))
     if rc:
         _check(rc, what)
@@ -315,14 +326,15 @@ def matmul_int8(q, q_scale, w, w_scale, offsets=None, rows=None, out=None, out_d
     return _product("matmul_int8", q, w, offsets, rows, out, out_dtype, stream, swiglu, q_scale, w_scale)
 
 
-def linear_int8(x, w, w_scale, offsets=None, rows=None, out=None, out_dtype=None, stream=None):
-    """x (bf16 or float32) quantised row by row and multiplied in 8-bit integers."""
-    return _product("linear_int8", x, w, offsets, rows, out, out_dtype, stream, False, None, w_scale, True)
+def linear_int8(x, w, w_scale, offsets=None, rows=None, out=None, out_dtype=None, stream=None, workspace=None):
+    """x (bf16 or float32) quantised row by row and multiplied in 8-bit integers.  workspace: uint8
+    scratch of msb_int8_linear_workspace_size bytes."""
+    return _product("linear_int8", x, w, offsets, rows, out, out_dtype, stream, False, None, w_scale, True, workspace)
 
 
-def swiglu_int8(x, w, w_scale, offsets=None, rows=None, out=None, stream=None):
+def swiglu_int8(x, w, w_scale, offsets=None, rows=None, out=None, stream=None, workspace=None):
     """linear_int8 for gate and up ([groups][2][n][k]) with SwiGLU."""
-    return _product("swiglu_int8", x, w, offsets, rows, out, None, stream, True, None, w_scale, True)
+    return _product("swiglu_int8", x, w, offsets, rows, out, None, stream, True, None, w_scale, True, workspace)
 
 
 # ------------------------------------------------------------------ combine, norms
