@@ -335,6 +335,7 @@ def test_workspaces_lie_in_a_row():
     gaps = torch.zeros(1 << 16, dtype=torch.uint8)[::2]
     x, w = torch.zeros(6, 32, dtype=torch.bfloat16), torch.zeros(8, 32, dtype=torch.int8)
     for f in (lambda ws: msb.linear_int8(x, w, torch.zeros(8), workspace=ws),
-              lambda ws: msb.swiglu_int8(x, w[None].expand(2, 8, 32).contiguous(), torch.zeros(2, 8), workspace=ws)):
+              lambda ws: msb.swiglu_int8(x, w[None].expand(2, 8, 32).contiguous(), torch.zeros(2, 8), workspace=ws),
+              lambda ws: msb.route(torch.zeros(4, 8), 2, workspace=ws)):
         with pytest.raises(ValueError, match="contiguous"):
             f(gaps)

@@ -161,6 +161,7 @@ def route(logits, top_e: int, renorm: bool = True, mask=None, out: Routing | Non
     need = _route_bytes(T, E)
     if mask is not None:
         _mask(mask, T)
+    given = None if workspace is None else _scratch(workspace)
     new = []
     if out is None:
         buf = _routing_buffer(T, E, top_e, need if workspace is None else 0, logits.device)
@@ -181,8 +182,8 @@ def route(logits, top_e: int, renorm: bool = True, mask=None, out: Routing | Non
             buf = torch.empty(max(1, need), dtype=torch.uint8, device=logits.device)
             new.append(buf)
             ws, nb = buf.data_ptr(), need
-    if workspace is not None:
-        ws, nb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if given:
+        ws, nb = given
     rc = lib.msb_route(logits.data_ptr(), code, ld, _ptr(mask), T, E, top_e, 1 if renorm else 0, *at, ws, nb,
                        _on(stream, dev, new))
     if rc:
