@@ -201,6 +201,68 @@ def test_float_outputs_keep_float_precision(msb):
         assert (got.double() - want).norm() < 1e-6 * want.norm()
 
 
+def whole(seed, *shape, most=2):
+    """bf16 whole numbers -most .. most: sums of their products below 2^24 are exact in float32,
+    in any order and however an addition is cut off."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-most, most + 1, shape, generator=g, device="cuda").to(torch.bfloat16)
+
+
+def long_weight(seed, lead, n, k, layout):
+    """whole() of [*lead][n][k], k or n contiguous on a pitch of whole 16 bytes."""
+    if layout == "k":
+        return whole(seed, *lead, n, (k + 7) // 8 * 8)[..., :k]
+    return whole(seed, *lead, k, (n + 7) // 8 * 8)[..., :n].transpose(-1, -2)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts,n,k", [([60, 0, 70], 300, 40000), ([100], 3000, 131136), ([70], 300, 140000)])
+def test_long_sums_lose_nothing(msb, counts, n, k, gather):
+    """k beyond one accumulator, with and without pairs that share it: sums of whole numbers come
+    out exact, rounded once to bf16, so that no part of k is lost or counted twice."""
+    import torch
+    R, E, T = sum(counts), len(counts), 40
+    offs = offsets_of(counts)
+    rows = torch.randint(-1, T + 1, (R,), device="cuda", dtype=torch.int32) if gather else None
+    x = whole(95, T if gather else R, k)
+    for layout in ("k", "n"):
+        w = long_weight(96, (E,), n, k, layout)
+        want, _ = product64(x, w, offs, rows)
+        assert torch.equal(msb.grouped_matmul(x, w, offs, rows=rows), want.bfloat16()), layout
+    w = long_weight(97, (E, 2), n, k, "k") * 2.0 ** -8  # gates of up to a few dozen
+    (g, _), (u, _) = (product64(x, w[:, p], offs, rows) for p in range(2))
+    want = torch.nn.functional.silu(g) * u
+    # exact sums: the exponential and the quotient (2^-16 at most), one rounding
+    within(msb.grouped_swiglu(x, w, offs, rows=rows), want, (BF16 + 2.0 ** -16) * want.abs() + 2.0 ** -117 * u.abs() + TINY)
+
+
+@pytest.mark.parametrize("counts,n,k", [([0, 100], 256, 1 << 18), ([100], 3000, 131136), ([64], 128, 1 << 20)])
+def test_long_sums_are_not_cut_off(msb, counts, n, k):
+    """Values of one sign, where every addition that is cut off errs the same way.  An accumulator's
+    32768 k take 2048 additions of less than 2^-23 each: the mean relative error of bf16 outputs stays
+    below 2.4e-4 (SwiGLU of large gates: twice that), plus the mean of N roundings of at most 2^-8
+    each, 6 standard deviations: 6 2^-8 / sqrt(3 N)."""
+    import torch
+    R, E = sum(counts), len(counts)
+    offs = offsets_of(counts)
+    gen = torch.Generator(device="cuda").manual_seed(98)
+    uni = lambda *s: torch.rand(*s, generator=gen, device="cuda")  # noqa: E731
+    x = (uni(R, k) * (1 + torch.linspace(0, 1, R, device="cuda"))[:, None]).bfloat16()
+    noise = 6 * BF16 / (3 * R * n) ** 0.5
+    for layout in ("k", "n"):
+        w = (uni(E, n, k) if layout == "k" else uni(E, k, n).transpose(1, 2)).bfloat16()
+        want, _ = product64(x, w, offs, None)
+        err = (msb.grouped_matmul(x, w, offs).double() - want) / want
+        assert err.mean().abs() < 2.4e-4 + noise, (layout, float(err.mean()))
+    if E == 2 or k >= 1 << 20:  # gate and up of the same values
+        w2 = torch.stack([w.contiguous()] * 2, 1)
+        x2 = x * 2.0 ** -9
+        g, _ = product64(x2, w, offs, None)
+        err = (msb.grouped_swiglu(x2, w2, offs).double() - g * g) / (g * g)
+        assert err.mean().abs() < 4.8e-4 + noise, float(err.mean())
+
+
 def test_swiglu_of_extreme_gates(msb):
     """Gates of +-300: silu is the gate itself and a zero of either sign, never NaN."""
     import torch

@@ -50,13 +50,18 @@ constexpr int kTileM = 256;       // weight rows per CTA pair
 constexpr int kStageBytes = 128;  // bytes of k per stage (one swizzle row)
 constexpr int kABytes = 128 * kStageBytes;  // one CTA's weight rows of a stage
 
-// Float outputs of bf16 products: the matrix unit cuts off each addition to its accumulator, by
-// about 1e-9 of the sum per k, always towards zero (measured: 1.5e-6 at k = 1536, 9e-6 at 8192).
-// That is far below bf16's rounding, but not float's, so there the accumulator takes
-// kExactStages stages (256 k, 2e-7) at a time and the epilogue sums them rounded to nearest.
-template <bool I8, bool F32>
-constexpr bool kExact = F32 && !I8;
-constexpr int kExactStages = 4;
+// bf16 products: the matrix unit cuts off each addition to its accumulator, an instruction's 16 k at
+// a time, by less than 2^-23 of the sum so far and always towards zero: for values of one sign by up
+// to 7.5e-9 of the sum per k (measured: 7e-9), for mixed signs far less (relative L2 1.5e-6 at k =
+// 1536, 9e-6 at 8192).  Float outputs have an accumulator take kExactStages stages (256 k, 2e-7) at
+// a time, bf16 ones kLongStages (32768 k: 2.4e-4 at most, a sixteenth of a bf16 rounding), and the
+// epilogue sums these parts rounded to nearest, which 64-row tiles have registers for (bf16, 2048 rows
+// by 1024 x 65536: 278 us, in one accumulator 198).  8-bit sums are exact.
+constexpr int kExactStages = 4, kLongStages = 512;
+
+// Stages summed in one accumulator; 0: all.  LONG: there are more than kLongStages.
+template <bool I8, bool F32, bool LONG>
+constexpr int kChunk = I8 ? 0 : F32 ? kExactStages : LONG ? kLongStages : 0;
 
 // Bytes between the staged rows of an epilogue warp's 32 bf16 channels: 64 and 16 more, so that
 // eight rows' 16-byte pieces fall into different banks.
@@ -283,10 +288,10 @@ __device__ __forceinline__ bool store_f32(const KArgs& a, typename Cfg<BN>::Shar
 // along the lanes of tensor memory and contiguously in the output, so 32 columns (rows of out)
 // at a time are turned through shared memory (transposing 8x8 stores) and leave as 16-byte
 // pieces; element by element where out is not aligned for that or the channels end.
-template <int BN, bool I8, bool GATED, int SPLIT>
+template <int BN, bool I8, bool GATED, bool LONG, int SPLIT>
 __device__ __forceinline__ bool store_bf16(const KArgs& a, typename Cfg<BN>::Shared& s, uint8_t* stages,
-                                           const Tile& tile, uint32_t tmem, int buf, uint32_t phase, uint32_t rank,
-                                           int part, int warp, int lane, int& met) {
+                                           const Tile& tile, uint32_t tmem, int& buf, uint32_t& phase, int nk,
+                                           uint32_t rank, int part, int warp, int lane, int& met) {
   constexpr int kCh = GATED ? 16 : 32;  // channels of this warp
   const int ch0 = GATED ? tile.m * 128 + (int)rank * 64 + warp * 16 : tile.m * kTileM + (int)rank * 128 + warp * 32;
   // scales of the accumulator rows lane / 4 + 8 i
@@ -300,21 +305,56 @@ __device__ __forceinline__ bool store_bf16(const KArgs& a, typename Cfg<BN>::Sha
                       : a.w_scale[(int64_t)tile.group * a.n + ch];
     }
   }
-  if (!wait_warp(&s.acc_full[buf], phase, &s.dead)) return false;
-  tc_fence_after();
+  // 32 columns of the accumulator in use
+  const auto columns = [&](int c0, uint32_t (&v)[2][16]) {
+    const uint32_t acc = tmem + buf * BN + ((uint32_t)(warp * 32) << 16);
+    tmem_ld16(acc + c0, v[0]);
+    tmem_ld16(acc + (16u << 16) + c0, v[1]);
+    tmem_ld_wait();
+  };
+  const auto next_acc = [&] {
+    if (++buf == 2) buf = 0, phase ^= 1;
+  };
+  float sum[LONG ? BN / 32 : 1][2][16];
+  if constexpr (LONG) {
+    static_assert(BN == 64, "the sums of a tile are held in registers");
+#pragma unroll
+    for (int j = 0; j < BN; ++j) sum[j >> 5][j >> 4 & 1][j & 15] = 0.f;
+    for (int i = 0; i < nk; i += kLongStages) {
+      if (!wait_warp(&s.acc_full[buf], phase, &s.dead)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int c0 = 0; c0 < BN; c0 += 32)
+        if (c0 < tile.rows) {
+          uint32_t v[2][16];
+          columns(c0, v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[c0 >> 5][j >> 4][j & 15] += __uint_as_float(v[j >> 4][j & 15]);
+        }
+      release_acc(s, buf, lane);
+      next_acc();
+    }
+  } else {
+    if (!wait_warp(&s.acc_full[buf], phase, &s.dead)) return false;
+    tc_fence_after();
+  }
   if (SPLIT > 1) {
     meet(met);
     if (part == 0) meet(met);
   }
-  const uint32_t acc = tmem + buf * BN + ((uint32_t)(warp * 32) << 16);
   uint8_t* const stage = s.out[warp];
   const int lim = a.n - ch0;  // channels of this warp that exist (may be <= 0)
-  for (int c0 = 0; c0 < tile.rows; c0 += 32) {
+#pragma unroll LONG ? BN / 32 : 1
+  for (int c0 = 0; c0 < (LONG ? BN : tile.rows); c0 += 32) {
+    if (LONG && c0 >= tile.rows) break;
     uint32_t v[2][16];
-    tmem_ld16(acc + c0, v[0]);
-    tmem_ld16(acc + (16u << 16) + c0, v[1]);
-    tmem_ld_wait();
-    if (c0 + 32 >= tile.rows) release_acc(s, buf, lane);
+    if constexpr (LONG) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j >> 4][j & 15] = __float_as_uint(sum[c0 >> 5][j >> 4][j & 15]);
+    } else {
+      columns(c0, v);
+      if (c0 + 32 >= tile.rows) release_acc(s, buf, lane);
+    }
     if (SPLIT > 1 && part > 0) {
       const uint32_t to = map_to(smem_addr(stages), rank);
 #pragma unroll
@@ -376,13 +416,15 @@ __device__ __forceinline__ bool store_bf16(const KArgs& a, typename Cfg<BN>::Sha
       }
     }
   }
+  if (!LONG) next_acc();
   return true;
 }
 
 // I8: 8-bit integers (else bf16).  MMAJOR: the weight's n runs contiguously (bf16 only).
-// GATED: rows of the weight tile alternate in eights, gate and up.  F32: float output.  SPLIT:
-// pairs that share a tile's k (with one tile per cluster and BN = 64).
-template <int BN, bool I8, bool MMAJOR, bool GATED, bool F32, int SPLIT>
+// GATED: rows of the weight tile alternate in eights, gate and up.  F32: float output.  LONG: bf16
+// sums of more than kLongStages stages (BN = 64).  SPLIT: pairs that share a tile's k (with one tile
+// per cluster and BN = 64).
+template <int BN, bool I8, bool MMAJOR, bool GATED, bool F32, bool LONG, int SPLIT>
 __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(Cfg<BN>::kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ RowMaps xmaps,
                    const KArgs a) {
@@ -467,7 +509,7 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(Cfg<BN>::kTh
     if (elect_one()) {
       int st = 0, buf = 0;
       uint32_t phase = 0, acc_phase = 0;
-      const int chunk = kExact<I8, F32> ? kExactStages : nk;  // stages summed in one accumulator
+      const int chunk = kChunk<I8, F32, LONG> ? kChunk<I8, F32, LONG> : nk;
       const uint32_t pa = smem_addr(stages);
       const uint64_t da0 = MMAJOR ? smem_desc(pa, kABytes / 2, 1024) : smem_desc(pa, 16, 1024);
       const uint64_t db0 = smem_desc(pa + kABytes, 16, 1024);
@@ -600,8 +642,8 @@ __global__ void __cluster_dims__(2 * SPLIT, 1, 1) __launch_bounds__(Cfg<BN>::kTh
       if constexpr (F32) {
         ok = store_f32<BN, I8, SPLIT>(a, s, stages, tile, tmem, buf, acc_phase, nk, rank, part, warp, lane, met);
       } else {
-        ok = store_bf16<BN, I8, GATED, SPLIT>(a, s, stages, tile, tmem, buf, acc_phase, rank, part, warp, lane, met);
-        if (++buf == 2) buf = 0, acc_phase ^= 1;
+        ok = store_bf16<BN, I8, GATED, LONG, SPLIT>(a, s, stages, tile, tmem, buf, acc_phase, nk, rank, part, warp, lane,
+                                                    met);
       }
     }
   }
@@ -688,9 +730,9 @@ bool row_maps(const GroupedArgs& a, RowMaps* maps) {
   return true;
 }
 
-template <int BN, bool I8, bool MMAJOR, bool GATED, bool F32, int SPLIT = 1>
+template <int BN, bool I8, bool MMAJOR, bool GATED, bool F32, int SPLIT = 1, bool LONG = false>
 int launch(const CUtensorMap& map, const RowMaps& xmaps, const KArgs& k, cudaStream_t st) {
-  const auto kernel = grouped_kernel<BN, I8, MMAJOR, GATED, F32, SPLIT>;
+  const auto kernel = grouped_kernel<BN, I8, MMAJOR, GATED, F32, LONG, SPLIT>;
   struct Device {
     std::once_flag once;
     cudaError_t rc;
@@ -713,6 +755,13 @@ int launch(const CUtensorMap& map, const RowMaps& xmaps, const KArgs& k, cudaStr
   return launch_early(kernel, 2 * SPLIT * clusters, Cfg<BN>::kThreads, Cfg<BN>::kSmemBytes, st, map, xmaps, k);
 }
 
+int stages_of(const KArgs& k) { return (k.kbytes + kStageBytes - 1) / kStageBytes; }
+
+// bf16 outputs whose accumulators would take more than kLongStages stages, with `split` parts of k.
+bool long_sums(const GroupedArgs& a, const KArgs& k, int split) {
+  return !a.i8 && !a.out_f32 && (stages_of(k) + split - 1) / split > kLongStages;
+}
+
 template <int BN, int SPLIT = 1>
 int launch_tile(const GroupedArgs& a, const CUtensorMap& map, const RowMaps& xmaps, const KArgs& k, cudaStream_t st) {
   if (a.i8) {
@@ -720,11 +769,16 @@ int launch_tile(const GroupedArgs& a, const CUtensorMap& map, const RowMaps& xma
     return a.out_f32 ? launch<BN, true, false, false, true, SPLIT>(map, xmaps, k, st)
                      : launch<BN, true, false, false, false, SPLIT>(map, xmaps, k, st);
   }
-  if (a.swiglu) return launch<BN, false, false, true, false, SPLIT>(map, xmaps, k, st);
-  if constexpr (BN == 64)
+  if constexpr (BN == 64) {
+    if (long_sums(a, k, SPLIT))
+      return a.swiglu     ? launch<BN, false, false, true, false, SPLIT, true>(map, xmaps, k, st)
+             : a.w_k != 1 ? launch<BN, false, true, false, false, SPLIT, true>(map, xmaps, k, st)
+                          : launch<BN, false, false, false, false, SPLIT, true>(map, xmaps, k, st);
     if (a.out_f32)
       return a.w_k != 1 ? launch<BN, false, true, false, true, SPLIT>(map, xmaps, k, st)
                         : launch<BN, false, false, false, true, SPLIT>(map, xmaps, k, st);
+  }
+  if (a.swiglu) return launch<BN, false, false, true, false, SPLIT>(map, xmaps, k, st);
   return a.w_k != 1 ? launch<BN, false, true, false, false, SPLIT>(map, xmaps, k, st)
                     : launch<BN, false, false, false, false, SPLIT>(map, xmaps, k, st);
 }
@@ -741,7 +795,7 @@ int resident_clusters() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mu);
   if (known[dev] == 0) {
-    const auto kernel = grouped_kernel<64, false, false, false, false, SPLIT>;
+    const auto kernel = grouped_kernel<64, false, false, false, false, false, SPLIT>;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2 * SPLIT, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
@@ -767,14 +821,14 @@ int resident_clusters() {
 // bf16 weight of 4096 x 4096 14.9 and 13.0 us, 512 x 4096 14.7 and 10.3, but 1024 x 1024 (16
 // stages) 6.8 and 8.1.
 int split_k(const GroupedArgs& a, const KArgs& k) {
-  const int64_t tiles = ((int64_t)a.out_rows + 63) / 64 * k.mtiles, stages = (k.kbytes + kStageBytes - 1) / kStageBytes;
-  if (a.groups != 1 || stages < 32) return 1;
+  const int64_t tiles = ((int64_t)a.out_rows + 63) / 64 * k.mtiles;
+  if (a.groups != 1 || stages_of(k) < 32) return 1;
   return tiles <= resident_clusters<4>() ? 4 : tiles <= resident_clusters<2>() ? 2 : 1;
 }
 
 // Rows of the tile that serves a product.
 int tile_rows(const GroupedArgs& a, const KArgs& k) {
-  if (a.out_f32 && !a.i8) return 64;  // sums in registers
+  if ((a.out_f32 && !a.i8) || long_sums(a, k, 1)) return 64;  // sums in registers
   const int64_t rows = a.out_rows, groups = std::min<int64_t>(a.groups, rows);
   // Few tiles: the smallest that one round of the pairs holds (one 4096 x 4096 bf16 weight, 64-,
   // 128- and 256-row tiles: 256 rows 15.5, 17.0, 25.3 us; 512 rows 25.9, 17.7, 26.0; 1024 rows
