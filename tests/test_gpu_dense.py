@@ -217,7 +217,44 @@ def long_weight(seed, lead, n, k, layout):
 
 
 @pytest.mark.parametrize("gather", [False, True])
-@pytest.mark.parametrize("counts,n,k", [([60, 0, 70], 300, 40000), ([100], 3000, 131136), ([70], 300, 140000)])
+@pytest.mark.parametrize("R,n,k", [(128, 4096, 2048), (64, 8192, 4100), (129, 2500, 2090), (200, 1000, 20000),
+                                   (3, 64, 20000), (17, 4100, 8192), (33, 9000, 4104)])
+def test_shared_k_loses_nothing(msb, R, n, k, gather):
+    """One weight whose tiles' k is shared by two or four pairs: whole numbers, exact sums (of 8-bit
+    values in float64), so that a stage that is lost or counted twice shows in every output."""
+    import torch
+    T = 40
+    rows = torch.randint(-1, T + 1, (R,), device="cuda", dtype=torch.int32) if gather else None
+    offs = offsets_of([R])
+    x = whole(92, T if gather else R, (k + 7) // 8 * 8)[:, :k]
+    for layout in ("k", "n"):
+        w = long_weight(93, (1,), n, k, layout)
+        want, _ = product64(x, w, offs, rows)
+        assert torch.equal(msb.grouped_matmul(x, w, rows=rows, out_dtype=torch.float32), want.float()), layout
+        assert torch.equal(msb.grouped_matmul(x, w, rows=rows), want.bfloat16()), layout
+    w = long_weight(94, (1, 2), n, k, "k").mul_(2.0 ** -6)  # gates of up to a few dozen
+    (g, _), (u, _) = (product64(x, w[:, p], offs, rows) for p in range(2))
+    want = torch.nn.functional.silu(g) * u
+    # exact sums: the exponential and the quotient (2^-16 at most), one rounding
+    within(msb.grouped_swiglu(x, w, rows=rows), want, (BF16 + 2.0 ** -16) * want.abs() + 2.0 ** -117 * u.abs() + TINY)
+    gen = torch.Generator(device="cuda").manual_seed(89)
+    eight = lambda *s: torch.randint(-128, 128, (*s, (k + 15) // 16 * 16), device="cuda", generator=gen).to(torch.int8)[..., :k]  # noqa: E731
+    q, w8 = eight(T if gather else R), eight(2, n)
+    one, ones = torch.ones(q.shape[0], device="cuda"), torch.ones(2, n, device="cuda")
+    want, _ = product64(q, w8[:1], offs, rows)
+    assert torch.equal(msb.matmul_int8(q, one, w8[0], ones[0], rows=rows, out_dtype=torch.float32), want.float())
+    # bf16: of the sum's float
+    assert torch.equal(msb.matmul_int8(q, one, w8[0], ones[0], rows=rows), want.float().bfloat16())
+    up, _ = product64(q, w8[1:], offs, rows)
+    scale = torch.full((2, n), 2.0 ** -18, device="cuda")  # gates of a few, exact but for the sums' float
+    g, u = want * 2.0 ** -18, up * 2.0 ** -18
+    h = torch.nn.functional.silu(g) * u
+    tol = (BF16 + 2.0 ** -16) * h.abs() + 2.2 * F32 * g.abs() * u.abs() + 2.0 ** -117 * u.abs() + TINY
+    within(msb.matmul_int8(q, one, w8, scale, rows=rows, swiglu=True), h, tol, "8-bit swiglu")
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts,n,k", [([60, 0, 70], 300, 40000), ([100], 3000, 131136), ([100], 1500, 131136), ([70], 300, 140000)])
 def test_long_sums_lose_nothing(msb, counts, n, k, gather):
     """k beyond one accumulator, with and without pairs that share it: sums of whole numbers come
     out exact, rounded once to bf16, so that no part of k is lost or counted twice."""
