@@ -108,7 +108,8 @@ int32_t msb_grouped_matmul(const void* x, int64_t ldx, int32_t x_rows, const int
                            int32_t out_type, int64_t ldo, void* stream);
 
 /* out[p][j] = silu(sum_i x[row(p)][i] * w[e][0][j][i]) * sum_i x[row(p)][i] * w[e][1][j][i];
- * bf16 out; everything else as msb_grouped_matmul. */
+ * bf16 out; everything else as msb_grouped_matmul.  silu is within (5 + 1.2 |g|) 2^-23 of its
+ * value for gates g down to -87, and zero below -87.4. */
 int32_t msb_grouped_swiglu(const void* x, int64_t ldx, int32_t x_rows, const int32_t* rows,
                            const int32_t* offsets, int32_t groups, int32_t out_rows,
                            const msb_group_weights* w, int32_t n, int32_t k, void* out,

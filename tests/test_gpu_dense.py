@@ -312,6 +312,22 @@ def test_swiglu_of_extreme_gates(msb):
     assert torch.equal(h[1], torch.zeros(3, device="cuda"))
 
 
+@pytest.mark.parametrize("R", [1, 40])
+def test_swiglu_over_the_range_of_gates(msb, R):
+    """Gates of -87 to 87 in quarters, exact: the exponential is within (2 + 1.173 |g|) 2^-23, its sum
+    with 1, the quotient and the product add 3 2^-23; one rounding to bf16."""
+    import torch
+    g = torch.arange(-348, 349, device="cuda") / 4.0
+    n = g.numel()
+    x = torch.ones((R, 8), device="cuda", dtype=torch.bfloat16)
+    w = torch.zeros((1, 2, n, 8), device="cuda", dtype=torch.bfloat16)
+    w[0, 0, :, 0], w[0, 0, :, 1] = g.floor().bfloat16(), (g - g.floor()).bfloat16()
+    w[0, 1, :, 2] = 2.0 ** 20
+    want = torch.nn.functional.silu(g.double()).expand(R, n) * 2.0 ** 20
+    tol = (BF16 + (5 + 1.173 * g.double().abs()) * 2 * F32) * want.abs()
+    within(msb.grouped_swiglu(x, w), want, tol)
+
+
 @pytest.mark.parametrize("R", [1, 2, 3, 4, 5, 7, 8])
 @pytest.mark.parametrize("k", [8, 33, 520, 2056, 4100])
 def test_few_rows(msb, R, k):

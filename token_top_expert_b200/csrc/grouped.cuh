@@ -66,9 +66,10 @@ __device__ __forceinline__ float value(uint32_t v, float row_scale, float scale)
   return __uint_as_float(v);
 }
 
-// silu(g) * u, with the approximate exponential and reciprocal (2^-20 relative; zero below
-// g = -87.3, where silu is under 2e-36): the exact quotient made the epilogue of a 256-row tile
-// 10 us.
+// silu(g) * u, with the approximate exponential, off by up to (2 + 1.173 |g|) 2^-23, and quotient
+// (2^-22): where g is negative silu is off by as much, 2^-18 at g = -20 and 2^-16 at -87, well below
+// bf16's 2^-8.  Zero below g = -87.3, where silu is under 2e-36.  The exact quotient made the
+// epilogue of a 256-row tile 10 us.
 __device__ __forceinline__ float gated(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
 inline KArgs kernel_args(const GroupedArgs& a) {
