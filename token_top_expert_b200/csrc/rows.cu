@@ -538,12 +538,16 @@ int norm_wide(const NormArgs& a, cudaStream_t st) {
   const int most = resident<block_norm_kernel<NT, V, HF32, YF32>, threads>();
   return launch_early(block_norm_kernel<NT, V, HF32, YF32>, std::min<int64_t>(blocks, most), threads, 0, st, a);
 }
+template <int NT, int V>
+int norm_wide_f32(const NormArgs& a, cudaStream_t st) {  // h, y or both in float
+  if (!a.h_f32) return norm_wide<NT, V, false, true>(a, st);
+  return a.y_f32 ? norm_wide<NT, V, true, true>(a, st) : norm_wide<NT, V, true, false>(a, st);
+}
 template <int NT, int W, int V>
 int norm_rows(const NormArgs& a, cudaStream_t st) {
   constexpr int threads = block_threads(NT);
   if constexpr (W == 8) {
-    if (a.h_f32) return a.y_f32 ? norm_wide<NT, V, true, true>(a, st) : norm_wide<NT, V, true, false>(a, st);
-    return a.y_f32 ? norm_wide<NT, V, false, true>(a, st) : norm_wide<NT, V, false, false>(a, st);
+    return a.h_f32 || a.y_f32 ? norm_wide_f32<NT, V>(a, st) : norm_wide<NT, V, false, false>(a, st);
   } else {
     const auto kernel = a.h_f32 ? (a.y_f32 ? block_norm_any_kernel<NT, V, true, true> : block_norm_any_kernel<NT, V, true, false>)
                                 : (a.y_f32 ? block_norm_any_kernel<NT, V, false, true>
@@ -624,7 +628,7 @@ int launch_block_norm(const NormArgs& a, cudaStream_t st) {
   // x 2048 2.6 and 2.1; float h, 8192 x 1024, 128 threads and a warp: 18.5 and 23.7).
   if (a.d <= 256) return MSB_NORM(32, 8, 1);
   if (a.d <= 512) return MSB_NORM(32, 8, 2);
-  if (a.d <= 1024) return f32 ? MSB_NORM(128, 8, 1) : MSB_NORM(32, 8, 4);
+  if (a.d <= 1024) return f32 ? norm_wide_f32<128, 1>(a, st) : norm_wide<32, 4, false, false>(a, st);
   if (a.d <= 2048) return rows >= kManyRows ? MSB_NORM(128, 8, 2) : MSB_NORM(256, 8, 1);
   if (a.d <= 4096) return MSB_NORM(256, 8, 2);
   if (a.d <= 8192) return MSB_NORM(512, 8, 2);
