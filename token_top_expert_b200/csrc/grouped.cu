@@ -808,8 +808,10 @@ int resident_clusters() {
     int n = 0;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<64>::kSmemBytes) !=
             cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess)
-      n = 0;
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;  // not kept: the next call tries again
+    }
     known[dev] = n > 0 ? n : -1;
   }
   return known[dev];

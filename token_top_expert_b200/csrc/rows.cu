@@ -509,9 +509,13 @@ int resident() {
   int dev = 0, sms = 0, per = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
   std::lock_guard<std::mutex> lock(mu);
-  if (!blocks[dev] && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0) == cudaSuccess)
-    blocks[dev] = sms * per;
+  if (!blocks[dev]) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0) == cudaSuccess)
+      blocks[dev] = sms * per;
+    else
+      cudaGetLastError();  // not kept: the next call asks again
+  }
   return blocks[dev] > 0 ? blocks[dev] : 148;
 }
 
