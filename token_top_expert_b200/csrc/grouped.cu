@@ -344,22 +344,13 @@ __device__ __forceinline__ bool store_bf16(const KArgs& a, typename Cfg<BN>::Sha
   }
   uint8_t* const stage = s.out[warp];
   const int lim = a.n - ch0;  // channels of this warp that exist (may be <= 0)
-#pragma unroll LONG ? BN / 32 : 1
-  for (int c0 = 0; c0 < (LONG ? BN : tile.rows); c0 += 32) {
-    if (LONG && c0 >= tile.rows) break;
-    uint32_t v[2][16];
-    if constexpr (LONG) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j >> 4][j & 15] = __float_as_uint(sum[c0 >> 5][j >> 4][j & 15]);
-    } else {
-      columns(c0, v);
-      if (c0 + 32 >= tile.rows) release_acc(s, buf, lane);
-    }
+  // 32 rows of out
+  const auto store_rows = [&](int c0, uint32_t (&v)[2][16]) {
     if (SPLIT > 1 && part > 0) {
       const uint32_t to = map_to(smem_addr(stages), rank);
 #pragma unroll
       for (int j = 0; j < 32; ++j) store_cluster(to + part_offset(part, warp, c0 + j, lane), v[j >> 4][j & 15]);
-      continue;
+      return;
     }
     if (SPLIT > 1)
       for (int q = 1; q < SPLIT; ++q)
@@ -415,8 +406,25 @@ __device__ __forceinline__ bool store_bf16(const KArgs& a, typename Cfg<BN>::Sha
         if (c < lim) out[(int64_t)row * a.ldo + c] = *reinterpret_cast<const uint16_t*>(stage + row * kOutPitch + 2 * c);
       }
     }
+  };
+  if constexpr (LONG) {
+#pragma unroll
+    for (int c0 = 0; c0 < BN; c0 += 32)
+      if (c0 < tile.rows) {
+        uint32_t v[2][16];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j >> 4][j & 15] = __float_as_uint(sum[c0 >> 5][j >> 4][j & 15]);
+        store_rows(c0, v);
+      }
+  } else {
+    for (int c0 = 0; c0 < tile.rows; c0 += 32) {
+      uint32_t v[2][16];
+      columns(c0, v);
+      if (c0 + 32 >= tile.rows) release_acc(s, buf, lane);
+      store_rows(c0, v);
+    }
+    next_acc();
   }
-  if (!LONG) next_acc();
   return true;
 }
 
@@ -733,25 +741,28 @@ bool row_maps(const GroupedArgs& a, RowMaps* maps) {
 template <int BN, bool I8, bool MMAJOR, bool GATED, bool F32, int SPLIT = 1, bool LONG = false>
 int launch(const CUtensorMap& map, const RowMaps& xmaps, const KArgs& k, cudaStream_t st) {
   const auto kernel = grouped_kernel<BN, I8, MMAJOR, GATED, F32, LONG, SPLIT>;
-  struct Device {
-    std::once_flag once;
-    cudaError_t rc;
-    int sms;
-  };
-  static Device devices[64];
-  int dev = 0;
+  static std::mutex mu;
+  static int known[64] = {};  // SMs of each device whose kernel has its shared memory
+  int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MSB_ECUDA;
-  Device& d = devices[dev];
-  std::call_once(d.once, [&] {
-    d.rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<BN>::kSmemBytes);
-    if (d.rc == cudaSuccess) d.rc = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-  });
-  if (d.rc != cudaSuccess) return MSB_ECUDA;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!known[dev]) {  // a failure is reported, not kept: the next call tries again
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<BN>::kSmemBytes) !=
+              cudaSuccess ||
+          cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return MSB_ECUDA;
+      }
+      known[dev] = sms;
+    }
+    sms = known[dev];
+  }
   // at most one pair (or cluster) per tile: pieces <= groups + rows / BN, and every piece has a row
   const int64_t most = ((int64_t)k.groups + k.out_rows / BN) * k.mtiles;
   const int64_t mine = (int64_t)k.out_rows * k.mtiles;
   const int64_t clusters = SPLIT > 1 ? (int64_t)(k.out_rows + BN - 1) / BN * k.mtiles
-                                     : std::min<int64_t>(d.sms / 2, std::min(most, mine));
+                                     : std::min<int64_t>(sms / 2, std::min(most, mine));
   return launch_early(kernel, 2 * SPLIT * clusters, Cfg<BN>::kThreads, Cfg<BN>::kSmemBytes, st, map, xmaps, k);
 }
 
