@@ -218,7 +218,8 @@ def long_weight(seed, lead, n, k, layout):
 
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("R,n,k", [(128, 4096, 2048), (64, 8192, 4100), (129, 2500, 2090), (200, 1000, 20000),
-                                   (3, 64, 20000), (17, 4100, 8192), (33, 9000, 4104)])
+                                   (3, 64, 20000), (17, 4100, 8192), (33, 9000, 4104), (128, 4096, 4104),
+                                   (129, 2500, 4200), (40, 5000, 8200), (64, 2048, 2560)])
 def test_shared_k_loses_nothing(msb, R, n, k, gather):
     """One weight whose tiles' k is shared by two or four pairs: whole numbers, exact sums (of 8-bit
     values in float64), so that a stage that is lost or counted twice shows in every output."""

@@ -828,15 +828,20 @@ int resident_clusters() {
   return known[dev];
 }
 
-// Pairs that share the k of each tile of 64 rows: one group whose tiles are so few that the
-// device holds all their clusters at once, and enough stages that the join (two meetings of the
-// cluster and the parts' way through shared memory, 2 us) pays.  Without and with it, 64 rows: a
-// bf16 weight of 4096 x 4096 14.9 and 13.0 us, 512 x 4096 14.7 and 10.3, but 1024 x 1024 (16
-// stages) 6.8 and 8.1.
+// Pairs that share the k of each tile of 64 rows: one group whose tiles are so few that the device
+// holds all their clusters at once, and enough stages that the join (two meetings of the cluster and
+// the parts' way through shared memory) pays.  Without and with it, 64 rows, cold bf16 weights n x k:
+// four pairs, 512 x 2304 8.9 and 8.6 us, 2048 x 2560 (40 stages) 9.7 and 9.9, 2048 x 3584 11.9 and
+// 10.6, 512 x 4096 12.4 and 9.6, 4096 x 4096 14.1 and 13.2, but 2048 x 2048 8.6 and 9.5, 1024 x 1024
+// 6.5 and 8.2; two pairs, 5120 x 4096 (64 stages) 14.7 and 14.1, 8192 x 4096 17.6 and 17.5, 5120 x
+// 8192 23.9 and 21.4, but 8192 x 3584 15.5 and 16.7; float outputs, 128 x 2048 (32 stages) 10.4 and
+// 10.2; 8 bits, 1024 x 5120 (40 stages) 9.5 and 9.4, 1024 x 4096 8.5 and 9.1.
 int split_k(const GroupedArgs& a, const KArgs& k) {
   const int64_t tiles = ((int64_t)a.out_rows + 63) / 64 * k.mtiles;
-  if (a.groups != 1 || stages_of(k) < 32) return 1;
-  return tiles <= resident_clusters<4>() ? 4 : tiles <= resident_clusters<2>() ? 2 : 1;
+  const int stages = stages_of(k);
+  if (a.groups != 1 || stages < (a.out_f32 && !a.i8 ? 32 : 40)) return 1;
+  if (tiles <= resident_clusters<4>()) return 4;
+  return stages >= 64 && tiles <= resident_clusters<2>() ? 2 : 1;
 }
 
 // Rows of the tile that serves a product.
