@@ -24,11 +24,14 @@
 //              board's power limit from 262 to 250 us, 8-bit ones from 135 to 120.
 //
 // What bounds it: weights from memory while the groups are small (64 tokens' gate and up, hidden
-// 2048 x 768 channels x 128 experts top-8, 96 to 120 us for 0.8 GB), then the way from L2 to
-// the SMs, about 80 bytes per nanosecond and SM (a 256 x 256 tile's stage of 64 KB takes its pair
-// 430 ns, the matrix instructions 270 of them): 4096 tokens' gate and up 205 to 250 us, 0.82 to
-// 1.0 PFLOP/s; bf16 8192^3 575 to 600 us, 1.83 to 1.91 PFLOP/s.  Long runs meet the board's
-// power limit and are slower by up to a fifth.
+// 2048 x 768 channels x 128 experts top-8, cold weights: 104 us for the 0.67 GB of the 106 experts in
+// use, 6.4 TB/s).  4096 tokens' gate and up read 0.8 GB of weights and take 205 us in short runs; the
+// same number of rows in equal groups of 256 180 us; in 8 groups, whose weights stay in L2, 139 (1.48
+// PFLOP/s; with one weight 136).  So it is the weights' way from memory while the matrix unit works,
+// then the uneven groups (1218 tiles of 171 rows on average, not 768 of 256; the busiest pair has
+// 6 % more than the mean).  Gathering costs 3 us of it, the records' strides and SwiGLU nothing.  bf16
+// 8192^3 takes 575 us (1.91 PFLOP/s) to 860 (1.28), by the clock that the board's power limit leaves;
+// long runs of all of these are slower by up to a fifth.
 #include <cuda.h>
 
 #include <algorithm>
@@ -103,7 +106,7 @@ struct RowMaps {
 // A bounded wait.  When it runs out, or another role of this CTA has given up, the caller
 // stops waiting for good and leaves through the common exit.  A poll may sleep up to kNapNs (it
 // ends with the phase all the same): with the default, far shorter one the waiting warps' polls
-// took issue slots (64 tokens' gate and up 98.0 us, 96.0 with it; 256 x 4096 by 4096 x 4096 15.6 and 14.1).
+// took issue slots (256 x 4096 by 4096 x 4096 17.0 us, 15.0 with it; 64 tokens' gate and up 105 either way).
 constexpr uint32_t kNapNs = 5000;
 __device__ bool wait_slow(uint64_t* bar, uint32_t parity, uint32_t* dead) {
   const uint64_t t0 = globaltimer_ns();
@@ -849,13 +852,13 @@ int tile_rows(const GroupedArgs& a, const KArgs& k) {
   if ((a.out_f32 && !a.i8) || long_sums(a, k, 1)) return 64;  // sums in registers
   const int64_t rows = a.out_rows, groups = std::min<int64_t>(a.groups, rows);
   // Few tiles: the smallest that one round of the pairs holds (one 4096 x 4096 bf16 weight, 64-,
-  // 128- and 256-row tiles: 256 rows 15.5, 17.0, 25.3 us; 512 rows 25.9, 17.7, 26.0; 1024 rows
-  // 47.1, 31.0, 28.2).
+  // 128- and 256-row tiles: 256 rows 15.2, 17.5, 26.8 us; 512 rows 23.4, 18.1, 28.3; 1024 rows
+  // 40.4, 29.9, 30.2).
   for (int bn = 64; bn <= 256; bn *= 2)
     if (k.mtiles * std::max(groups, (rows + bn - 1) / bn) <= kPairs) return bn;
   // Many: by the rows of a group, on average (gate and up of hidden 2048 x 768 channels x 128
-  // experts; bf16, 16 rows 126, 126, 132 us; 64 rows 144, 133, 137; 128 rows 216, 169, 153; 8
-  // bits, 16 rows 66, 68, 71; 64 rows 79, 71, 74; 128 rows 138, 92, 92).
+  // experts, cold weights; bf16, 16 rows 124, 126, 132 us; 64 rows 140, 133, 139; 128 rows 188, 157,
+  // 151; 8 bits, 16 rows 69, 68, 72; 64 rows 78, 73, 76; 128 rows 107, 89, 85).
   return rows <= 32 * groups ? 64 : rows <= 64 * groups ? 128 : 256;
 }
 
